@@ -1,4 +1,4 @@
-"""ctypes loader for libmoe.so: the C ABI declared in include/moe.h and include/moe_adamw.h.
+"""ctypes loader for libmoe.so: the C ABI declared in include/moe*.h.
 
 Argument marshalling only.  There is no fallback: if the library has not been
 built (``__graft_entry__.build()`` or ``python -m top_softmax_router_gb300.build``)
@@ -24,7 +24,9 @@ MOE_ERR_NOT_BUILT = -7
 
 KERNEL_CLASSES = ["router_logits", "router_topk", "plan", "gather", "gemm_gateup", "gemm_down", "combine",
                   "gemm_dact", "gemm_dw", "gemm_dx", "unpermute", "router_dw", "zero", "hop_plan", "finalize",
-                  "adamw", "ce_logits", "ce_merge", "ce_dlogit", "ce_dx", "ce_dw", "route_grad"]
+                  "adamw", "ce_logits", "ce_merge", "ce_dlogit", "ce_dx", "ce_dw", "route_grad", "norm_fwd",
+                  "norm_bwd", "embed_fwd", "embed_sort", "embed_bwd", "scores_fwd", "scores_bwd", "distill_prep",
+                  "distill_logits", "distill_loss", "distill_d", "distill_dx", "distill_dw"]
 
 # Every symbol include/*.h declares.
 EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "moe_forward", "moe_backward",
@@ -33,7 +35,10 @@ EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "mo
            "moe_route_noalloc",
            "moe_hop_rows_worst_case", "moe_hops_workspace_bytes", "moe_forward_hops", "moe_backward_hops",
            "moe_set_gemm_form", "moe_set_launch_chaining", "moe_set_dispatch", "moe_adamw_staging_bytes", "moe_adamw_offload_step", "moe_adamw_step",
-           "moe_ce_workspace_bytes", "moe_ce_forward", "moe_ce_backward", "moe_ce_last_stats"]
+           "moe_ce_workspace_bytes", "moe_ce_forward", "moe_ce_backward", "moe_ce_last_stats",
+           "moe_layernorm_workspace_bytes", "moe_layernorm_forward", "moe_layernorm_backward",
+           "moe_embed_workspace_bytes", "moe_embed_forward", "moe_embed_backward",
+           "moe_scores_workspace_bytes", "moe_scores_forward", "moe_scores_backward"]
 
 MOE_GEMM_AUTO, MOE_GEMM_SINGLE, MOE_GEMM_PAIR = 0, 1, 2
 MOE_DISPATCH_GATHER, MOE_DISPATCH_ON_LOAD = 0, 1
@@ -54,6 +59,19 @@ class AdamwHparams(ctypes.Structure):
 
 class CeConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "V", "P")]
+
+
+class LayerNormConfig(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class EmbedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "V", "H", "padding_idx")] + [("scale", ctypes.c_float)]
+
+
+class ScoresConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "E", "k", "groups", "topk_groups", "group_top", "score",
+                                              "renormalize")] + [("scale", ctypes.c_float)]
 
 
 class CeStats(ctypes.Structure):
@@ -85,6 +103,7 @@ def load() -> ctypes.CDLL:
         cfgp = ctypes.POINTER(MoeConfig)
         hpp = ctypes.POINTER(AdamwHparams)
         cep = ctypes.POINTER(CeConfig)
+        lnp, emp, scp = ctypes.POINTER(LayerNormConfig), ctypes.POINTER(EmbedConfig), ctypes.POINTER(ScoresConfig)
         sig = {
             "moe_workspace_bytes": [cfgp, ctypes.POINTER(SZ), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
             "moe_route": [cfgp, P, P, P, P, P, P, SZ, P],
@@ -117,6 +136,15 @@ def load() -> ctypes.CDLL:
             "moe_ce_forward": [cep, P, P, P, P, P, P, P, SZ, P],
             "moe_ce_backward": [cep, P, P, P, P, P, P, P, P, SZ, P],
             "moe_ce_last_stats": [ctypes.POINTER(CeStats)],
+            "moe_layernorm_workspace_bytes": [lnp, ctypes.POINTER(SZ)],
+            "moe_layernorm_forward": [lnp, P, I64, P, P, P, P, P, I32, I32, P],
+            "moe_layernorm_backward": [lnp, P, I64, P, P, P, P, I64, P, P, P, I32, I32, P, SZ, P],
+            "moe_embed_workspace_bytes": [emp, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
+            "moe_embed_forward": [emp, P, I32, P, P, I32, P, SZ, P],
+            "moe_embed_backward": [emp, P, I32, P, I64, I32, P, I32, P, SZ, P],
+            "moe_scores_workspace_bytes": [scp, ctypes.POINTER(SZ)],
+            "moe_scores_forward": [scp, P, I64, I32, P, P, P, P, P, SZ, P],
+            "moe_scores_backward": [scp, P, I64, I32, P, P, P, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)

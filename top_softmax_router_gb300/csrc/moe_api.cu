@@ -58,7 +58,10 @@ const char* kKernelNames[MOE_K_COUNT] = {"router_logits", "router_topk", "plan",
                                          "gemm_dw",       "gemm_dx",     "unpermute", "router_dw",
                                          "zero",          "hop_plan",    "finalize",  "adamw",
                                          "ce_logits",     "ce_merge",    "ce_dlogit", "ce_dx",
-                                         "ce_dw",         "route_grad"};
+                                         "ce_dw",         "route_grad",  "norm_fwd",  "norm_bwd",
+                                         "embed_fwd",     "embed_sort",  "embed_bwd", "scores_fwd",
+                                         "scores_bwd",    "distill_prep", "distill_logits", "distill_loss",
+                                         "distill_d",     "distill_dx",  "distill_dw"};
 
 cudaEvent_t take_event() {
   if (!g_free_events.empty()) {

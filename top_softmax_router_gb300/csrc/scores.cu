@@ -1,0 +1,493 @@
+// Routing to experts from given logits: scores, balance bias, groups, top-k, weights, and the gradient
+// (include/moe_scores.h).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/moe.h"
+#include "../../include/moe_scores.h"
+#include "ops_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kWarps = 8;   // rows a block holds at a time
+
+// Keys order floats as unsigned integers: 0 = not a candidate, 1 = NaN, then -inf upwards.  -0 counts as 0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (v != v) return 1u;
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+struct Params {
+  const float* bias;
+  int N, E, k, groups, topk_groups, group_top, group_size;
+  uint32_t group_inv;   // ceil(2^20 / group_size): e / group_size = (e group_inv) >> 20 for e < 1024
+  bool sigmoid, renormalize;
+  float scale;
+};
+
+// What a row's scores are computed from: l -> s.
+struct RowScore {
+  float m, sum;      // softmax: maximum and sum of exp(l - m)
+  bool sigmoid;
+  __device__ __forceinline__ float of(float l) const {
+    if (sigmoid) return 1.0f / (1.0f + expf(-l));
+    if (m == -INFINITY) return l == l ? 0.0f : l;
+    return expf(l - m) / sum;
+  }
+};
+
+// exp(l - m) of a chosen expert, relative to itself within a few 2^-24 however far l is from m: what the
+// subtraction rounds off comes back as a factor.
+__device__ __forceinline__ float chosen_exp(float l, float m) {
+  if (l == -INFINITY) return 0.0f;
+  const float d = l - m, b = d - l, off = (l - (d - b)) - (m + b);
+  return expf(d) * (1.0f + off);
+}
+
+// fp64 scores of a row, for values that fp32 cannot order.
+struct ExactScore {
+  double m, sum;
+  bool sigmoid;
+  __device__ __forceinline__ double of(float l) const {
+    if (sigmoid) return 1.0 / (1.0 + exp(-(double)l));
+    if (isinf(m) && m < 0) return l == l ? 0.0 : (double)l;
+    return exp((double)l - m) / sum;
+  }
+};
+
+// (Reads the row again: taking the logits by reference would keep them in local memory for every row.)
+template <class T>
+__device__ __noinline__ ExactScore exact_score(const T* lr, float m, bool sigmoid, int E) {
+  ExactScore x = {(double)m, 0.0, sigmoid};
+  if (sigmoid) return x;
+  double s = 0.0;
+  for (int e = threadIdx.x & 31; e < E; e += 32) s += exp((double)to_f32<T>(lr[e]) - x.m);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+  x.sum = s;
+  return x;
+}
+
+// The value an expert is chosen by, in fp64.
+template <class T>
+__device__ __noinline__ double exact_value(const ExactScore x, const T* lr, const float* bias, int e) {
+  return x.of(to_f32<T>(lr[e])) + (bias ? (double)bias[e] : 0.0);
+}
+
+// The group's score from the values c[0 .. size) of its experts, spread over `width` lanes (a power of two):
+// the sum of its `top` largest.  NaN values are passed over.
+template <class F>
+__device__ __forceinline__ F group_score(const F* c, int size, int sub, int width, int top) {
+  F m1 = (F)-INFINITY, m2 = (F)-INFINITY;
+  for (int i = sub; i < size; i += width) {
+    const F v = c[i];
+    if (v > m1) m2 = m1, m1 = v;
+    else if (v > m2) m2 = v;
+  }
+  for (int off = 1; off < width; off <<= 1) {
+    const F o1 = __shfl_xor_sync(kFull, m1, off), o2 = __shfl_xor_sync(kFull, m2, off);
+    const F hi = m1 > o1 ? m1 : o1, lo = m1 > o1 ? o1 : m1;
+    const F second = m1 > o1 ? m2 : o2;
+    m1 = hi;
+    m2 = lo > second ? lo : second;
+  }
+  const F s = top == 2 && size > 1 ? m1 + m2 : m1;
+  return s == s ? s : (F)-INFINITY;
+}
+
+// One warp a row.  Lane t holds experts t, t + 32, ..  The k choices are k rounds of a warp maximum over
+// integer keys (redux), then a warp minimum over the expert ids that have it.  Two fp32 values can be in the
+// wrong order only if they lie within `window` of each other; a round that finds such a candidate beside
+// its choice compares those candidates in fp64 (unless their logit and bias are equal, when the tie rule
+// decides).
+template <class T, int PER>
+__global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __restrict__ logits, int64_t ld, Params p,
+                                                                int32_t* __restrict__ topk_idx,
+                                                                float* __restrict__ weights,
+                                                                int32_t* __restrict__ counts) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ double sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
+  int* hist = reinterpret_cast<int*>(sm);                                       // [E] choices of this block
+  double* vals = sm + (E + 1) / 2 + (int64_t)warp * (p.groups > 1 ? E : 0);      // [E] values of the row's groups
+  if (counts) {
+    for (int e = threadIdx.x; e < E; e += 32 * kWarps) hist[e] = 0;
+    __syncthreads();
+  }
+  int width = 32;                 // lanes a group: 32 / (groups rounded up to a power of two)
+  while (width > 1 && width * p.groups > 32) width >>= 1;
+  for (int64_t row = (int64_t)blockIdx.x * kWarps + warp; row < p.N; row += (int64_t)gridDim.x * kWarps) {
+    const T* lr = logits + row * ld;
+    float l[PER];
+    uint32_t key[PER];
+    float m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = q * 32 + lane;
+      l[q] = e < E ? to_f32<T>(lr[e]) : -INFINITY;
+      m = fmaxf(m, l[q]);
+    }
+    RowScore score = {m, 1.0f, p.sigmoid};
+    if (!p.sigmoid) {
+      m = score.m = key_value(__reduce_max_sync(kFull, order_key(m)));
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (q * 32 + lane < E) s += expf(l[q] - m);
+      s = warp_sum(s);
+      score.sum = m == -INFINITY ? 1.0f : s;   // every logit masked: all scores are 0
+    }
+    // Without a bias c grows with l, so the logits themselves order the experts exactly (window 0).
+    // Else |error of c| <= |error of s| + 2^-24 |c|: a sigmoid is at most 2^-22 off (expf 2^-23 relative, an
+    // addition and a division of 2^-24 each; s <= 1), a softmax at most 42 x 2^-24 of the row's largest
+    // score (the exponent's rounding x e^-x <= 0.37, expf, the division and a sum of up to 32 + 5 steps).
+    // Twice that for a pair, and a margin of two.
+    const float window0 = p.bias ? (p.sigmoid ? 0x1p-20f : 0x1p-17f / score.sum) : 0.0f;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = q * 32 + lane;
+      key[q] = e < E ? order_key(p.bias ? score.of(l[q]) + __ldg(p.bias + e) : l[q]) : 0u;
+    }
+    if (p.groups > 1) {
+      // values the groups are scored by: c, or s where there is no bias (the logit itself when only the
+      // largest counts)
+      const bool by_logit = !p.bias && p.group_top == 1;
+      const float wide = by_logit ? 0.0f : 2.0f * (p.sigmoid ? 0x1p-20f : 0x1p-17f / score.sum);
+      float* v32 = reinterpret_cast<float*>(vals);
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int e = q * 32 + lane;
+        if (e < E) v32[e] = by_logit ? l[q] : p.bias ? (key[q] > 1u ? key_value(key[q]) : NAN) : score.of(l[q]);
+      }
+      __syncwarp();
+      const int g = lane / width, sub = lane % width;
+      const bool mine = g < p.groups;
+      const float gs = group_score<float>(v32 + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+      const float w = wide + fabsf(gs) * (wide > 0.0f ? 0x1p-21f : 0.0f);
+      // rank of the group: how many are surely before it, and how many may be
+      int before = 0, sure = 0, maybe = 0;
+      for (int h = 0; h < p.groups; ++h) {
+        const float o = __shfl_sync(kFull, gs, h * width);
+        before += o > gs || (o == gs && h < g);
+        sure += o > gs + w;
+        maybe += h != g && o >= gs - w;
+      }
+      bool open = mine && before < p.topk_groups;
+      const bool unsure = mine && wide > 0.0f && sure < p.topk_groups && maybe >= p.topk_groups;
+      if (__any_sync(kFull, unsure)) {
+        const ExactScore exact = exact_score<T>(lr, m, p.sigmoid, E);
+        __syncwarp();
+        for (int e = lane; e < E; e += 32) vals[e] = exact_value<T>(exact, lr, p.bias, e);
+        __syncwarp();
+        const double gd =
+            group_score<double>(vals + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+        before = 0;
+        for (int h = 0; h < p.groups; ++h) {
+          const double o = __shfl_sync(kFull, gd, h * width);
+          before += o > gd || (o == gd && h < g);
+        }
+        open = mine && before < p.topk_groups;
+      }
+      const uint32_t open_lanes = __ballot_sync(kFull, open);
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const uint32_t eg = ((uint32_t)(q * 32 + lane) * p.group_inv) >> 20;
+        if (!((open_lanes >> (eg * width & 31)) & 1u)) key[q] = 0u;
+      }
+    }
+    // k rounds
+    int my_e = 0;
+    uint32_t best = 0u;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) best = max(best, key[q]);
+    for (int j = 0; j < p.k; ++j) {
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      int q_first = 0;
+#pragma unroll
+      for (int q = PER - 1; q >= 0; --q)
+        if (key[q] == top) q_first = q;
+      int e = __reduce_min_sync(kFull, best == top ? q_first * 32 + lane : 0x7fffffff);
+      if (p.bias && top > 1u) {
+        const float tv = key_value(top);
+        const uint32_t near_key = order_key(tv - (window0 + fabsf(tv) * 0x1p-22f));
+        bool near = false;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) near |= key[q] >= near_key && q * 32 + lane != e;
+        if (__any_sync(kFull, near)) {
+          const float le = to_f32<T>(lr[e]), be = p.bias[e];
+          bool other = false;
+#pragma unroll
+          for (int q = 0; q < PER; ++q)
+            if (key[q] >= near_key) other |= l[q] != le || p.bias[q * 32 + lane] != be;
+          if (__any_sync(kFull, other)) {
+            const ExactScore exact = exact_score<T>(lr, m, p.sigmoid, E);
+            uint32_t mine = 0;
+#pragma unroll
+            for (int q = 0; q < PER; ++q) mine |= (key[q] >= near_key ? 1u : 0u) << q;
+            double bv = -INFINITY;
+            int bq = 0x7fffffff;
+            for (; mine; mine &= mine - 1) {
+              const int i = (__ffs(mine) - 1) * 32 + lane;
+              const double v = exact_value<T>(exact, lr, p.bias, i);
+              if (bq == 0x7fffffff || v > bv) bv = v, bq = i;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+              const double ov = __shfl_xor_sync(kFull, bv, off);
+              const int oq = __shfl_xor_sync(kFull, bq, off);
+              if (oq != 0x7fffffff && (bq == 0x7fffffff || ov > bv || (ov == bv && oq < bq))) bv = ov, bq = oq;
+            }
+            e = bq;
+          }
+        }
+      }
+      if (lane == j) my_e = e;
+      if ((e & 31) == lane) {
+        best = 0u;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          if (q == (e >> 5)) key[q] = 0u;
+          best = max(best, key[q]);
+        }
+      }
+    }
+    // weights, the sum in slot order
+    const float ls = lane < p.k ? to_f32<T>(lr[my_e]) : -INFINITY;
+    float s = 0.0f, total = 1.0f;
+    if (p.sigmoid || !p.renormalize) {
+      if (lane < p.k) s = score.of(ls);
+    } else {
+      s = chosen_exp(ls, key_value(__reduce_max_sync(kFull, order_key(ls))));   // the row's sum cancels
+    }
+    if (p.renormalize) {
+      total = 0.0f;
+      for (int j = 0; j < p.k; ++j) total += __shfl_sync(kFull, s, j);
+    }
+    if (lane < p.k) {
+      topk_idx[row * p.k + lane] = my_e;
+      weights[row * p.k + lane] = total == 0.0f ? 0.0f : p.scale * (s / total);
+      if (counts) atomicAdd(hist + my_e, 1);
+    }
+  }
+  if (counts) {
+    // integer adds: the order does not change the result
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 32 * kWarps)
+      if (hist[e]) atomicAdd(counts + e, hist[e]);
+  }
+}
+
+// One warp a row: the chosen experts' gradients (and, for a softmax that is not renormalised, everyone's) are
+// put together in shared memory and the row is stored whole.
+template <class T, int VEC>
+__global__ void __launch_bounds__(32 * kWarps) scores_bwd_kernel(const T* __restrict__ logits, int64_t ld, Params p,
+                                                                const int32_t* __restrict__ topk_idx,
+                                                                const float* __restrict__ dweights,
+                                                                T* __restrict__ dlogits, int* status) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ float rows[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
+  float* out = rows + warp * ((E + 3) / 4 * 4);
+  const bool dense = !p.sigmoid && !p.renormalize;
+  for (int64_t row = (int64_t)blockIdx.x * kWarps + warp; row < p.N; row += (int64_t)gridDim.x * kWarps) {
+    const T* lr = logits + row * ld;
+    const bool slot = lane < p.k;
+    const int e = slot ? topk_idx[row * p.k + lane] : 0;
+    const bool ok = slot && e >= 0 && e < E;
+    if (slot && !ok) report(status, MOE_ERR_DEVICE_CHECK, 601);
+    const float dw = ok ? dweights[row * p.k + lane] : 0.0f;
+    const float l = ok ? to_f32<T>(lr[e]) : -INFINITY;
+    float dl;   // of the chosen expert
+    if (dense) {
+      float m = -INFINITY, s = 0.0f;
+      for (int i = lane; i < E; i += 32) {
+        const float v = to_f32<T>(lr[i]);
+        out[i] = v;
+        m = fmaxf(m, v);
+      }
+      m = key_value(__reduce_max_sync(kFull, order_key(m)));
+      for (int i = lane; i < E; i += 32) {
+        const float v = m == -INFINITY ? (out[i] == out[i] ? 0.0f : out[i]) : expf(out[i] - m);
+        out[i] = v;
+        s += v;
+      }
+      s = warp_sum(s);
+      const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+      __syncwarp();
+      const float se = ok ? out[e] * inv : 0.0f;
+      const float all = warp_sum(ok ? p.scale * dw * se : 0.0f);
+      dl = se * (p.scale * dw - all);
+      __syncwarp();
+      for (int i = lane; i < E; i += 32) out[i] = -out[i] * inv * all;
+    } else {
+      for (int i = lane; i < E; i += 32) out[i] = 0.0f;
+      float s, rest;   // share of the renormalised sum (or the score), and the derivative's other factor
+      if (p.sigmoid) {
+        s = ok ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+        rest = ok ? 1.0f / (1.0f + expf(l)) : 0.0f;
+      } else {   // renormalised softmax: a softmax over the chosen logits alone
+        const float m = key_value(__reduce_max_sync(kFull, order_key(ok ? l : -INFINITY)));
+        s = chosen_exp(l, m);   // l is -inf where there is no expert
+        rest = 1.0f;
+      }
+      if (p.renormalize) {
+        const float total = warp_sum(s);
+        s = total == 0.0f ? 0.0f : s / total;
+        dl = p.scale * s * (dw - warp_sum(dw * s)) * rest;
+      } else {
+        dl = p.scale * s * dw * rest;
+      }
+    }
+    __syncwarp();
+    if (ok) out[e] = dl;
+    __syncwarp();
+    T* dst = dlogits + row * E;
+    for (int i = lane * VEC; i < E; i += 32 * VEC) {
+      float f[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] = out[i + j];
+      *reinterpret_cast<Pack<T, VEC>*>(dst + i) = pack<T, VEC>(f);
+    }
+    __syncwarp();
+  }
+}
+
+int scores_validate(const moe_scores_config* c) {
+  if (!c || c->N < 0 || c->E <= 0 || c->k <= 0 || c->groups <= 0 || c->topk_groups <= 0 ||
+      (c->group_top != 1 && c->group_top != 2) || (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) ||
+      (c->renormalize != 0 && c->renormalize != 1) || !std::isfinite(c->scale))
+    return MOE_ERR_INVALID_ARG;
+  if (c->E > 1024 || c->groups > 32 || c->E % c->groups != 0 || c->topk_groups > c->groups || c->k > 32 ||
+      c->k > c->topk_groups * (c->E / c->groups))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+Params params(const moe_scores_config& c, const float* bias) {
+  Params p = {};
+  p.bias = bias;
+  p.N = c.N;
+  p.E = c.E;
+  p.k = c.k;
+  p.groups = c.topk_groups == c.groups ? 1 : c.groups;   // all open: no group is closed
+  p.topk_groups = c.topk_groups;
+  p.group_top = c.group_top;
+  p.group_size = c.E / c.groups;
+  p.group_inv = (uint32_t)(((1 << 20) + p.group_size - 1) / p.group_size);
+  p.sigmoid = c.score == MOE_SCORE_SIGMOID;
+  p.renormalize = c.renormalize != 0;
+  p.scale = c.scale;
+  return p;
+}
+
+unsigned row_blocks(int N) {
+  const int64_t need = ((int64_t)N + kWarps - 1) / kWarps;
+  return (unsigned)std::min<int64_t>(need, (int64_t)device_sm_count() * 8);
+}
+
+template <class F>
+cudaError_t with_per(int E, F&& f) {
+  const int per = (E + 31) / 32;
+  if (per <= 1) return f(std::integral_constant<int, 1>{});
+  if (per <= 2) return f(std::integral_constant<int, 2>{});
+  if (per <= 4) return f(std::integral_constant<int, 4>{});
+  if (per <= 8) return f(std::integral_constant<int, 8>{});
+  if (per <= 12) return f(std::integral_constant<int, 12>{});
+  if (per <= 16) return f(std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 32>{});
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_scores_workspace_bytes(const moe_scores_config* cfg, size_t* bytes) {
+  const int v = scores_validate(cfg);
+  if (v != MOE_OK) return v;
+  if (bytes) *bytes = sizeof(WsHeader);
+  return MOE_OK;
+}
+
+int moe_scores_forward(const moe_scores_config* cfg, const void* logits, int64_t ld, int32_t type,
+                       const float* bias, int32_t* topk_idx, float* weights, int32_t* counts, void* ws,
+                       size_t ws_bytes, void* stream) {
+  const int v = scores_validate(cfg);
+  if (v != MOE_OK) return v;
+  const moe_scores_config& c = *cfg;
+  if (!known_type(type) || ld < c.E || !ws || !aligned_to(ws, 16) || !aligned_to(bias, 4) || !aligned_to(counts, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c.N > 0 && (!logits || !topk_idx || !weights || !aligned_to(logits, type_size(type)) ||
+                  !aligned_to(topk_idx, 4) || !aligned_to(weights, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (counts) {
+    const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)c.E * 4, s);
+    if (e != cudaSuccess) return record_cuda_error(e, "clear counts");
+  }
+  if (c.N == 0) return MOE_OK;
+  const Params p = params(c, bias);
+  return timed_launch(MOE_K_SCORES_FWD, "expert scores", s, [&] {
+    return with_type(type, [&](auto tv) {
+      using T = decltype(tv);
+      return with_per(c.E, [&](auto per) {
+        auto kern = scores_fwd_kernel<T, decltype(per)::value>;
+        // [E] counters, then [E] values a warp where there are groups: at most 4 KB + 64 KB
+        const size_t smem = ((size_t)(c.E + 1) / 2 + (p.groups > 1 ? (size_t)kWarps * c.E : 0)) * 8;
+        if (smem > 48 * 1024) {
+          const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+          if (e != cudaSuccess) return e;
+        }
+        return launch_pdl(kern, dim3(row_blocks(c.N)), dim3(32 * kWarps), smem, s, static_cast<const T*>(logits), ld, p,
+                          topk_idx, weights, counts);
+      });
+    });
+  });
+}
+
+int moe_scores_backward(const moe_scores_config* cfg, const void* logits, int64_t ld, int32_t type,
+                        const int32_t* topk_idx, const float* dweights, void* dlogits, void* ws, size_t ws_bytes,
+                        void* stream) {
+  const int v = scores_validate(cfg);
+  if (v != MOE_OK) return v;
+  const moe_scores_config& c = *cfg;
+  if (!known_type(type) || ld < c.E || !ws || !aligned_to(ws, 16)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.N == 0) return MOE_OK;
+  const size_t ts = type_size(type);
+  if (!logits || !topk_idx || !dweights || !dlogits || !aligned_to(logits, ts) || !aligned_to(dlogits, ts) ||
+      !aligned_to(topk_idx, 4) || !aligned_to(dweights, 4))
+    return MOE_ERR_INVALID_ARG;
+  const Params p = params(c, nullptr);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* status = static_cast<int*>(ws);
+  return timed_launch(MOE_K_SCORES_BWD, "expert scores backward", s, [&] {
+    return with_type(type, [&](auto tv) {
+      using T = decltype(tv);
+      auto go = [&](auto vv) {
+        const size_t smem = (size_t)kWarps * ((c.E + 3) / 4 * 4) * 4;   // at most 32 KB
+        return launch_pdl(scores_bwd_kernel<T, decltype(vv)::value>, dim3(row_blocks(c.N)), dim3(32 * kWarps), smem, s,
+                          static_cast<const T*>(logits), ld, p, topk_idx, dweights, static_cast<T*>(dlogits), status);
+      };
+      if (c.E % 4 == 0 && aligned_to(dlogits, 4 * ts)) return go(std::integral_constant<int, 4>{});
+      return go(std::integral_constant<int, 1>{});
+    });
+  });
+}
+
+}  // extern "C"
