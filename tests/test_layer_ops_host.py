@@ -102,6 +102,34 @@ def test_scores_arguments(lib):
     assert bwd(n=0) == SMALL
 
 
+@pytest.mark.parametrize("cfg,code", [
+    ((-1, 64, 10, 2, 1, 1.0), INVALID), ((4, 64, 10, 2, 1, 0.0), INVALID), ((4, 64, 10, 2, 1, -1.0), INVALID),
+    ((4, 64, 10, 2, 1, float("nan")), INVALID), ((4, 64, 10, 2, 1, 1e-45), INVALID), ((4, 65, 10, 2, 1, 1.0), SHAPE),
+    ((4, 64, 0, 2, 1, 1.0), SHAPE), ((4, 64, (1 << 20) + 1, 2, 1, 1.0), SHAPE), ((4, 64, 10, 257, 1, 1.0), SHAPE),
+    ((4, 64, 10, 0, 1, 1.0), SHAPE), ((4, 64, 10, 2, 11, 1.0), SHAPE), ((4, 64, 10, 2, 0, 1.0), SHAPE),
+    ((4, 64, 1 << 20, 256, 1, 1.0), 0)])
+def test_distill_shapes(lib, cfg, code):
+    assert lib.load().moe_distill_workspace_bytes(ref(lib.DistillConfig(*cfg)), None, None) == code
+
+
+def test_distill_arguments(lib):
+    L, c = lib.load(), lib.DistillConfig(4, 64, 10, 2, 1, 1.0)
+
+    def fwd(X=FAKE, W=FAKE, ids=FAKE, t=FAKE, loss=FAKE, lse=FAKE, ws=FAKE, n=1 << 24):
+        return L.moe_distill_forward(ref(c), X, W, ids, t, loss, lse, None, ws, n, None)
+
+    assert fwd(X=None) == fwd(W=None) == fwd(ids=None) == fwd(t=ODD) == fwd(loss=None) == fwd(lse=None) == INVALID
+    assert fwd(X=ctypes.c_void_p(4104)) == fwd(ws=None) == INVALID
+    assert fwd(n=256) == SMALL
+
+    def bwd(X=FAKE, W=FAKE, ids=FAKE, lse=FAKE, g=FAKE, dX=FAKE, dW=FAKE, t=1, ws=FAKE, n=1 << 24):
+        return L.moe_distill_backward(ref(c), X, W, ids, FAKE, lse, g, dX, dW, t, ws, n, None)
+
+    assert bwd(X=None) == bwd(W=ODD) == bwd(ids=None) == bwd(lse=None) == bwd(g=None) == bwd(dX=None) == INVALID
+    assert bwd(dW=ctypes.c_void_p(4104)) == bwd(t=2) == bwd(ws=None) == INVALID
+    assert bwd(n=256) == SMALL
+
+
 def test_python_refuses_host_tensors_types_and_shapes(lib):
     import top_softmax_router_gb300 as M
     ln = M.LayerNorm(M.LayerNormConfig(N=4, H=8), device="cpu")

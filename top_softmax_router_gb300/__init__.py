@@ -8,4 +8,5 @@ from .ce import *  # noqa: F401,F403
 from .norm import *  # noqa: F401,F403
 from .embed import *  # noqa: F401,F403
 from .scores import *  # noqa: F401,F403
+from .distill import *  # noqa: F401,F403
 from .autograd import *  # noqa: F401,F403

@@ -38,7 +38,8 @@ EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "mo
            "moe_ce_workspace_bytes", "moe_ce_forward", "moe_ce_backward", "moe_ce_last_stats",
            "moe_layernorm_workspace_bytes", "moe_layernorm_forward", "moe_layernorm_backward",
            "moe_embed_workspace_bytes", "moe_embed_forward", "moe_embed_backward",
-           "moe_scores_workspace_bytes", "moe_scores_forward", "moe_scores_backward"]
+           "moe_scores_workspace_bytes", "moe_scores_forward", "moe_scores_backward",
+           "moe_distill_workspace_bytes", "moe_distill_forward", "moe_distill_backward"]
 
 MOE_GEMM_AUTO, MOE_GEMM_SINGLE, MOE_GEMM_PAIR = 0, 1, 2
 MOE_DISPATCH_GATHER, MOE_DISPATCH_ON_LOAD = 0, 1
@@ -74,6 +75,10 @@ class ScoresConfig(ctypes.Structure):
                                               "renormalize")] + [("scale", ctypes.c_float)]
 
 
+class DistillConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "V", "K", "P")] + [("temperature", ctypes.c_float)]
+
+
 class CeStats(ctypes.Structure):
     _fields_ = [("strips", ctypes.c_int32), ("strip_classes", ctypes.c_int32), ("strip_bytes", ctypes.c_int64),
                 ("strip_bound_bytes", ctypes.c_int64), ("partial_bytes", ctypes.c_int64),
@@ -104,6 +109,7 @@ def load() -> ctypes.CDLL:
         hpp = ctypes.POINTER(AdamwHparams)
         cep = ctypes.POINTER(CeConfig)
         lnp, emp, scp = ctypes.POINTER(LayerNormConfig), ctypes.POINTER(EmbedConfig), ctypes.POINTER(ScoresConfig)
+        dsp = ctypes.POINTER(DistillConfig)
         sig = {
             "moe_workspace_bytes": [cfgp, ctypes.POINTER(SZ), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
             "moe_route": [cfgp, P, P, P, P, P, P, SZ, P],
@@ -145,6 +151,9 @@ def load() -> ctypes.CDLL:
             "moe_scores_workspace_bytes": [scp, ctypes.POINTER(SZ)],
             "moe_scores_forward": [scp, P, I64, I32, P, P, P, P, P, SZ, P],
             "moe_scores_backward": [scp, P, I64, I32, P, P, P, P, SZ, P],
+            "moe_distill_workspace_bytes": [dsp, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
+            "moe_distill_forward": [dsp, P, P, P, P, P, P, P, P, SZ, P],
+            "moe_distill_backward": [dsp, P, P, P, P, P, P, P, P, I32, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)

@@ -1,0 +1,408 @@
+// Distillation of a vocabulary head from a teacher's top logits (include/moe_distill.h).
+//
+// The entries (row, class, probability q) are put into buckets of 32 rows x 256 classes first, so that the GEMM
+// epilogues find those of their tile: the forward reads their logits out of tensor memory, the backward subtracts q
+// at their places.  Everything else of d is one exponential.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/moe.h"
+#include "../../include/moe_distill.h"
+#include "head_gemm.cuh"
+#include "ops_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxK = 256;
+constexpr int kGroup = 32;        // rows of a bucket
+// Row tiles of a band: the ~76 clusters at work then hold 8 x ~10 tiles, 36 MB of operands at H = 4096.
+constexpr int kHeadBand = 8;
+
+// One block a group of 32 rows, four rows a warp: q of each entry, equal classes of a row joined at the first of
+// them (class[j] = -1 for every other), the row's sum of q log q, and the group's entries by class tile.
+__global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __restrict__ ids,
+                                                           const float* __restrict__ teacher,
+                                                           const float* __restrict__ dloss, float* __restrict__ q_out,
+                                                           int32_t* __restrict__ class_out, float* __restrict__ qlogq,
+                                                           float* __restrict__ coef, int* __restrict__ bucket,
+                                                           uint32_t* __restrict__ entry, int N, int V, int K, int tiles,
+                                                           float T, int* status) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int count[];            // [tiles + 1]
+  __shared__ int s_class[8][kMaxK];
+  __shared__ float s_q[8][kMaxK];
+  __shared__ int scratch[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = blockIdx.x, r0 = group * kGroup;
+  for (int i = threadIdx.x; i <= tiles; i += 256) count[i] = 0;
+  __syncthreads();
+  for (int k = 0; k < 4; ++k) {
+    const int row = r0 + warp * 4 + k;
+    if (row >= N) break;                    // the same for the whole warp
+    const int64_t base = (int64_t)row * K;
+    float m = -INFINITY;
+    for (int j = lane; j < K; j += 32) {
+      const int c = ids[base + j];
+      if (c < -1 || c >= V) report(status, MOE_ERR_DEVICE_CHECK, 711);
+      const float t = teacher[base + j];
+      const bool there = c >= 0 && c < V && t != -INFINITY;
+      s_class[warp][j] = there ? c : -1;
+      s_q[warp][j] = t;
+      if (there) m = fmaxf(m, t);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float sum = 0.0f, dot = 0.0f;
+    for (int j = lane; j < K; j += 32) {
+      const bool there = s_class[warp][j] >= 0;
+      const float x = there ? (s_q[warp][j] - m) / T : 0.0f;
+      const float e = there ? expf(x) : 0.0f;
+      s_q[warp][j] = e;
+      sum += e;
+      dot = fmaf(e, x, dot);
+    }
+    sum = warp_sum(sum);
+    dot = warp_sum(dot);
+    const bool some = sum != 0.0f;          // the largest entry's e is 1
+    if (lane == 0) {
+      qlogq[row] = some ? dot / sum - logf(sum) : 0.0f;
+      if (coef) coef[row] = some ? dloss[row] * T : 0.0f;
+    }
+    __syncwarp();
+    for (int j = lane; j < K; j += 32) {
+      int c = s_class[warp][j];
+      float q = 0.0f;
+      if (c >= 0) {
+        bool first = true;
+        for (int i = 0; i < j; ++i) first &= s_class[warp][i] != c;
+        if (first)
+          for (int i = j; i < K; ++i) q += s_class[warp][i] == c ? s_q[warp][i] : 0.0f;
+        else
+          c = -1;
+      }
+      q_out[base + j] = some ? q / sum : 0.0f;
+      class_out[base + j] = c;
+      if (c >= 0) atomicAdd(count + (c >> 8), 1);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  // exclusive scan of the counts; thread t owns a run of tiles
+  const int per = (tiles + 255) / 256, t0 = threadIdx.x * per, t1 = min(tiles, t0 + per);
+  int own = 0;
+  for (int t = t0; t < t1; ++t) own += count[t];
+  int x = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  int at = x - own;
+  for (int w = 0; w < warp; ++w) at += scratch[w];
+  at += group * kGroup * K;
+  int* b = bucket + (int64_t)group * (tiles + 1);
+  for (int t = t0; t < t1; ++t) {
+    const int c = count[t];
+    b[t] = at;
+    count[t] = at;
+    at += c;
+  }
+  if (t0 < tiles && t1 == tiles) b[tiles] = at;
+  __syncthreads();
+  // an entry's place within its bucket does not change any result
+  for (int k = 0; k < 4; ++k) {
+    const int row = r0 + warp * 4 + k;
+    if (row >= N) break;
+    for (int j = lane; j < K; j += 32) {
+      const int c = class_out[(int64_t)row * K + j];
+      if (c >= 0) entry[atomicAdd(count + (c >> 8), 1)] = (uint32_t)(row - r0) | (uint32_t)(c & 255) << 5 | (uint32_t)j << 13;
+    }
+  }
+}
+
+// Folds (m2, z2) into (m, z): z counts in units of 2^m.
+__device__ __forceinline__ void fold2(float& m, float& z, float m2, float z2) {
+  const float mn = fmaxf(m, m2);
+  if (mn == -INFINITY) return;
+  z = z * exp2f(m - mn) + z2 * exp2f(m2 - mn);
+  m = mn;
+}
+
+// 32 rows a block: lse from the half tiles' pairs (warp w takes half tiles w, w + 8, .. in order, then the warps are
+// folded in order), and the loss from the entries' logits.
+__global__ void __launch_bounds__(256) distill_loss_kernel(const float* __restrict__ part_m,
+                                                           const float* __restrict__ part_z,
+                                                           const float* __restrict__ entry_logit,
+                                                           const float* __restrict__ q,
+                                                           const int32_t* __restrict__ cls,
+                                                           const float* __restrict__ qlogq, float* __restrict__ loss,
+                                                           float* __restrict__ lse, int N, int K, int parts, float T) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float sm[8][32], sz[8][32], s_lse[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * 32, row = r0 + lane;
+  float m = -INFINITY, z = 0.0f;
+  if (row < N)
+    for (int i = warp; i < parts; i += 8) fold2(m, z, part_m[(int64_t)i * N + row], part_z[(int64_t)i * N + row]);
+  sm[warp][lane] = m;
+  sz[warp][lane] = z;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < 8; ++w) fold2(m, z, sm[w][lane], sz[w][lane]);
+    const float l = m * 0.6931471805599453f + logf(z);
+    s_lse[lane] = l;
+    if (row < N) lse[row] = l;
+  }
+  __syncthreads();
+  const float inv_t = 1.0f / T;
+  for (int k = 0; k < 4; ++k) {
+    const int i = warp * 4 + k;
+    if (r0 + i >= N) break;
+    const int64_t base = (int64_t)(r0 + i) * K;
+    float a = 0.0f;
+    bool some = false;
+    for (int j = lane; j < K; j += 32)
+      if (cls[base + j] >= 0) {
+        a = fmaf(q[base + j], s_lse[i] - entry_logit[base + j] * inv_t, a);
+        some = true;
+      }
+    a = warp_sum(a);
+    some = __any_sync(0xffffffffu, some);
+    if (lane == 0) loss[r0 + i] = some ? T * T * (qlogq[r0 + i] + a) : 0.0f;
+  }
+}
+
+// sum_n loss[n] / N in a fixed order: strided sums of the threads, then a tree over the block.
+__global__ void __launch_bounds__(1024) distill_mean_kernel(const float* __restrict__ loss, float* out, int N) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s[32];
+  float a = 0.0f;
+  for (int i = threadIdx.x; i < N; i += 1024) a += loss[i];
+  a = warp_sum(a);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = a;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    a = warp_sum(s[threadIdx.x]);
+    if (threadIdx.x == 0) *out = N > 0 ? a / (float)N : 0.0f;
+  }
+}
+
+struct DistillLayout {
+  int groups, tiles;     // groups of 32 rows; class tiles of 256
+  int Vs, S;             // classes a strip (a multiple of 256), strips
+  size_t q, cls, qlogq, coef, bucket, entry;
+  size_t part_m, part_z, entry_logit, fwd_total;
+  size_t d, acc, bwd_total;
+};
+
+DistillLayout distill_layout(const moe_distill_config& c) {
+  DistillLayout L = {};
+  const int64_t N = c.N, V = c.V, K = c.K;
+  L.groups = (int)((N + kGroup - 1) / kGroup);
+  L.tiles = (int)((V + 255) / 256);
+  L.Vs = (int)(((V + c.P - 1) / c.P + 255) / 256 * 256);
+  L.S = (int)((V + L.Vs - 1) / L.Vs);
+  size_t o = align256(sizeof(WsHeader));
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align256(o + bytes);
+    return at;
+  };
+  L.q = take((size_t)N * K * 4);
+  L.cls = take((size_t)N * K * 4);
+  L.qlogq = take((size_t)N * 4);
+  L.coef = take((size_t)N * 4);
+  L.bucket = take((size_t)L.groups * (L.tiles + 1) * 4);
+  L.entry = take((size_t)L.groups * kGroup * K * 4);
+  const size_t common = o;
+  L.part_m = take((size_t)N * 2 * L.tiles * 4);
+  L.part_z = take((size_t)N * 2 * L.tiles * 4);
+  L.entry_logit = take((size_t)N * K * 4);
+  L.fwd_total = o;
+  o = common;
+  L.d = take((size_t)N * L.Vs * 2);
+  L.acc = take(L.S > 1 ? (size_t)N * c.H * 4 : 0);
+  L.bwd_total = o;
+  return L;
+}
+
+int distill_validate(const moe_distill_config* c) {
+  if (!c || c->N < 0 || c->H < 0 || c->V < 0 || c->K < 0 || c->P < 0 || !(c->temperature > 0.0f) ||
+      !std::isfinite(c->temperature) || !std::isfinite(1.0f / c->temperature))
+    return MOE_ERR_INVALID_ARG;
+  if (c->H < 64 || c->H % 64 != 0 || c->V < 1 || c->V > (1 << 20) || c->P < 1 || c->P > c->V || c->K < 1 ||
+      c->K > kMaxK)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)c->N * c->K > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+bool ok16(const void* p) { return p != nullptr && aligned_to(p, 16); }
+bool ok4(const void* p) { return p != nullptr && aligned_to(p, 4); }
+
+int prepare(const moe_distill_config& c, const DistillLayout& L, const int32_t* ids, const float* teacher,
+            const float* dloss, uint8_t* w, cudaStream_t s) {
+  return timed_launch(MOE_K_DISTILL_PREP, "distill entries", s, [&] {
+    const size_t smem = (size_t)(L.tiles + 1) * 4;   // at most 16 KB
+    return launch_pdl(distill_prep_kernel, dim3(L.groups), dim3(256), smem, s, ids, teacher, dloss,
+                      reinterpret_cast<float*>(w + L.q), reinterpret_cast<int32_t*>(w + L.cls),
+                      reinterpret_cast<float*>(w + L.qlogq),
+                      dloss ? reinterpret_cast<float*>(w + L.coef) : static_cast<float*>(nullptr),
+                      reinterpret_cast<int*>(w + L.bucket), reinterpret_cast<uint32_t*>(w + L.entry), c.N, c.V, c.K,
+                      L.tiles, c.temperature, reinterpret_cast<int*>(w));
+  });
+}
+
+HeadGemm head_params(const moe_distill_config& c, const DistillLayout& L, uint8_t* w) {
+  HeadGemm p = {};
+  p.band = kHeadBand;
+  p.status = reinterpret_cast<int*>(w);
+  p.limit_ns = wait_limit_ns();
+  p.to_log2 = (float)(1.4426950408889634 / (double)c.temperature);
+  p.tiles_all = L.tiles;
+  p.K = c.K;
+  p.bucket = reinterpret_cast<const int*>(w + L.bucket);
+  p.entry = reinterpret_cast<const uint32_t*>(w + L.entry);
+  p.q = reinterpret_cast<const float*>(w + L.q);
+  return p;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_distill_workspace_bytes(const moe_distill_config* cfg, size_t* fwd_bytes, size_t* bwd_bytes) {
+  const int v = distill_validate(cfg);
+  if (v != MOE_OK) return v;
+  const DistillLayout L = distill_layout(*cfg);
+  if (fwd_bytes) *fwd_bytes = L.fwd_total;
+  if (bwd_bytes) *bwd_bytes = L.bwd_total;
+  return MOE_OK;
+}
+
+int moe_distill_forward(const moe_distill_config* cfg, const uint16_t* X, const uint16_t* W, const int32_t* ids,
+                        const float* teacher, float* loss, float* lse, float* loss_mean, void* ws, size_t ws_bytes,
+                        void* stream) {
+  int v = distill_validate(cfg);
+  if (v != MOE_OK) return v;
+  const moe_distill_config& c = *cfg;
+  const DistillLayout L = distill_layout(c);
+  if (!ok16(ws) || !ok16(W) || !aligned_to(loss_mean, 4)) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < L.fwd_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.N > 0 && (!ok16(X) || !ok4(ids) || !ok4(teacher) || !ok4(loss) || !ok4(lse))) return MOE_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  if (c.N > 0) {
+    CUtensorMap a, b;
+    if (!make_map_2d(&a, X, c.H, c.N, 64, 128) || !make_map_2d(&b, W, c.H, c.V, 64, 128))
+      return record_cuda_error(cudaErrorInvalidValue, "distill tensor maps");
+    if ((v = prepare(c, L, ids, teacher, nullptr, w, s)) != MOE_OK) return v;
+    HeadGemm p = head_params(c, L, w);
+    p.M = c.N;
+    p.N = c.V;
+    p.nk = c.H / GEMM_BK;
+    p.part_m = reinterpret_cast<float*>(w + L.part_m);
+    p.part_z = reinterpret_cast<float*>(w + L.part_z);
+    p.entry_logit = reinterpret_cast<float*>(w + L.entry_logit);
+    if ((v = timed_launch(MOE_K_DISTILL_LOGITS, "distill logits", s, [&] {
+           return launch_head_gemm<HEAD_LSE, false, false>(a, b, p, device_sm_count(), s);
+         })) != MOE_OK)
+      return v;
+    if ((v = timed_launch(MOE_K_DISTILL_LOSS, "distill loss", s, [&] {
+           return launch_pdl(distill_loss_kernel, dim3(L.groups), dim3(256), 0, s, static_cast<const float*>(p.part_m),
+                             static_cast<const float*>(p.part_z), static_cast<const float*>(p.entry_logit), p.q,
+                             reinterpret_cast<const int32_t*>(w + L.cls),
+                             reinterpret_cast<const float*>(w + L.qlogq), loss, lse, c.N, c.K, 2 * L.tiles,
+                             c.temperature);
+         })) != MOE_OK)
+      return v;
+  }
+  if (!loss_mean) return MOE_OK;
+  return timed_launch(MOE_K_DISTILL_LOSS, "distill mean", s, [&] {
+    return launch_pdl(distill_mean_kernel, dim3(1), dim3(1024), 0, s, static_cast<const float*>(loss), loss_mean, c.N);
+  });
+}
+
+int moe_distill_backward(const moe_distill_config* cfg, const uint16_t* X, const uint16_t* W, const int32_t* ids,
+                         const float* teacher, const float* lse, const float* dloss, uint16_t* dX, void* dW,
+                         int32_t dw_type, void* ws, size_t ws_bytes, void* stream) {
+  int v = distill_validate(cfg);
+  if (v != MOE_OK) return v;
+  const moe_distill_config& c = *cfg;
+  const DistillLayout L = distill_layout(c);
+  if (!ok16(ws) || !ok16(W) || !ok16(dW) || (dw_type != MOE_TYPE_BF16 && dw_type != MOE_TYPE_F32))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < L.bwd_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c.N == 0) {
+    const cudaError_t e = cudaMemsetAsync(dW, 0, (size_t)c.V * c.H * type_size(dw_type), s);
+    return e == cudaSuccess ? MOE_OK : record_cuda_error(e, "clear dW");
+  }
+  if (!ok16(X) || !ok4(ids) || !ok4(teacher) || !ok4(lse) || !ok4(dloss) || !ok16(dX)) return MOE_ERR_INVALID_ARG;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const int sms = device_sm_count();
+  uint16_t* d = reinterpret_cast<uint16_t*>(w + L.d);
+  float* acc = reinterpret_cast<float*>(w + L.acc);
+  CUtensorMap xk, xm;   // X with K along the row (logits) and across the rows (dW)
+  if (!make_map_2d(&xk, X, c.H, c.N, 64, 128) || !make_map_2d(&xm, X, c.H, c.N, 64, 64))
+    return record_cuda_error(cudaErrorInvalidValue, "distill tensor maps");
+  if ((v = prepare(c, L, ids, teacher, dloss, w, s)) != MOE_OK) return v;
+  for (int st = 0; st < L.S; ++st) {
+    const int v0 = st * L.Vs, width = std::min(L.Vs, c.V - v0);
+    const uint16_t* Ws = W + (size_t)v0 * c.H;
+    CUtensorMap wk, wm, dk, dm;
+    if (!make_map_2d(&wk, Ws, c.H, width, 64, 128) || !make_map_2d(&wm, Ws, c.H, width, 64, 64) ||
+        !make_map_2d_strided(&dk, d, width, c.N, L.Vs, 64, 128) || !make_map_2d_strided(&dm, d, width, c.N, L.Vs, 64, 64))
+      return record_cuda_error(cudaErrorInvalidValue, "distill tensor maps");
+    HeadGemm p = head_params(c, L, w);   // d of the strip
+    p.M = c.N;
+    p.N = width;
+    p.nk = c.H / GEMM_BK;
+    p.tile0 = v0 / 256;
+    p.lse = lse;
+    p.coef = reinterpret_cast<const float*>(w + L.coef);
+    p.d = d;
+    p.ldd = L.Vs;
+    if ((v = timed_launch(MOE_K_DISTILL_D, "distill d", s, [&] {
+           return launch_head_gemm<HEAD_D, false, false>(xk, wk, p, sms, s);
+         })) != MOE_OK)
+      return v;
+    HeadGemm x = head_params(c, L, w);   // dX (+)= d W_strip, in bf16 after the last strip
+    x.M = c.N;
+    x.N = c.H;
+    x.nk = (width + GEMM_BK - 1) / GEMM_BK;
+    x.add = st > 0 ? acc : nullptr;
+    if (st + 1 < L.S) x.out32 = acc;
+    else x.out16 = dX;
+    x.ldo = c.H;
+    if ((v = timed_launch(MOE_K_DISTILL_DX, "distill dX", s, [&] {
+           return launch_head_gemm<HEAD_OUT, false, true>(dk, wm, x, sms, s);
+         })) != MOE_OK)
+      return v;
+    HeadGemm g = head_params(c, L, w);   // dW_strip = d^T X
+    g.M = width;
+    g.N = c.H;
+    g.nk = (int)(((int64_t)c.N + GEMM_BK - 1) / GEMM_BK);
+    if (dw_type == MOE_TYPE_BF16) g.out16 = static_cast<uint16_t*>(dW) + (size_t)v0 * c.H;
+    else g.out32 = static_cast<float*>(dW) + (size_t)v0 * c.H;
+    g.ldo = c.H;
+    if ((v = timed_launch(MOE_K_DISTILL_DW, "distill dW", s, [&] {
+           return launch_head_gemm<HEAD_OUT, true, true>(dm, xm, g, sms, s);
+         })) != MOE_OK)
+      return v;
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,376 @@
+// Dense GEMM on CTA pairs for the distillation head: C [M, N] = A [M, K] B [N, K]^T, bf16 in, fp32 accumulators in
+// tensor memory, with the head's epilogues.
+//
+// A cluster of two CTAs owns a 256 x 256 tile: each loads its 128 rows of A and half of the tile's 256 rows of B (64
+// of K at a time, 32 KB a stage, 6 stages); the even CTA issues tcgen05.mma.cta_group::2 (M = 256, N = 256, K = 16),
+// which leaves rows 0..127 in its own tensor memory and rows 128..255 in its peer's.  Two accumulators of 256 columns
+// let the epilogue of a tile run under the main loop of the next.
+//
+// Warps of a CTA (320 threads): 0 loads, 1 issues the MMAs (even CTA), 2..9 are the epilogue: two for each quarter of
+// the tensor memory's lanes, one for each half of the tile's columns.
+//
+// Every wait is bounded (wait_bounded): a wait that runs out sets the workspace status, and both CTAs leave.
+#pragma once
+
+#include "common.cuh"
+#include "gemm_kernel.cuh"   // store_bf16x32, GEMM_BK
+
+namespace moe {
+
+enum HeadEpi : int {
+  HEAD_LSE = 0,   // (max, sum of 2^..) of each row over each 128-class half tile; the entries' logits
+  HEAD_D = 1,     // d in bf16
+  HEAD_OUT = 2    // C: fp32 or bf16, added to an fp32 matrix of the same shape where there is one
+};
+
+struct HeadGemm {
+  int M, N, nk;              // rows, columns, K blocks of 64
+  int tiles_m, tiles_n, band;
+  int* status;
+  int64_t limit_ns;
+  // HEAD_LSE, HEAD_D
+  float to_log2;             // log2(e) / T: logits in units of T ln 2
+  int tile0;                 // class tile (of 256) of column 0
+  int tiles_all, K;          // class tiles of the vocabulary; entries a row
+  const int* bucket;         // [ceil(M / 32)][tiles_all + 1]: first entry of (32 rows, class tile)
+  const uint32_t* entry;     // row in group | column in tile << 5 | slot << 13
+  float* part_m;             // [2 tiles_n][M]
+  float* part_z;
+  float* entry_logit;        // [M][K]
+  const float* lse;          // [M], natural
+  const float* coef;         // [M]: g T where the row has entries, else 0
+  const float* q;            // [M][K]
+  uint16_t* d;               // [M][ldd]
+  int ldd;
+  // HEAD_OUT
+  const float* add;          // [M][ldo] or NULL
+  float* out32;              // [M][ldo] or NULL
+  uint16_t* out16;           // [M][ldo] or NULL
+  int ldo;
+};
+
+struct HeadSmem {
+  static constexpr int HALF = 128 * GEMM_BK * 2;       // 16 KB: this CTA's rows of A, or its half of B
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int STAGES = 6;
+  static constexpr int BAR = STAGES * STAGE;
+  static constexpr int TOTAL = BAR + 256 + 1024;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+};
+
+// 2^x, relative error at most 2^-22 (PTX ex2.approx); 0 for large negative x.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One fp32 column of tensor memory: each thread gets its lane's value.
+__device__ __forceinline__ float tc_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  return __uint_as_float(r);
+}
+
+// The epilogue of one warp: rows row0 + lane (valid below p.M), the columns c0 .. c0 + 127 of column tile nt.
+template <int EPI>
+__device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int nt, int half, uint32_t tacc, int lane) {
+  const int row = row0 + lane;
+  const bool ok = row < p.M;
+  const int n0 = nt * 256;
+  const int c0 = half * 128, c1 = min(c0 + 128, p.N - n0);
+  float v[32];
+  if constexpr (EPI == HEAD_LSE) {
+    // m: running maximum of y = logit x to_log2; z: sum of 2^(y - m), rescaled when m grows
+    float m = -INFINITY, z = 0.0f;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {
+      tc_ld32(tacc + c, v);
+      const int valid = c1 - c;
+      float cm = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < valid) cm = fmaxf(cm, v[j]);
+      const float mn = fmaxf(m, cm * p.to_log2);
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < valid) s += exp2_fast(fmaf(v[j], p.to_log2, -mn));
+      z = fmaf(z, exp2_fast(m - mn), s);
+      m = mn;
+    }
+    if (ok) {
+      p.part_m[(int64_t)(2 * nt + half) * p.M + row] = m;
+      p.part_z[(int64_t)(2 * nt + half) * p.M + row] = z;
+    }
+  } else if constexpr (EPI == HEAD_D) {
+    const float coef = ok ? p.coef[row] : 0.0f;
+    const float l = ok ? p.lse[row] * 1.4426950408889634f : 0.0f;
+    uint16_t* d = p.d + (int64_t)row * p.ldd + n0;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {
+      tc_ld32(tacc + c, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = coef == 0.0f ? 0.0f : coef * exp2_fast(fmaf(v[j], p.to_log2, -l));
+      if (ok) store_bf16x32(d + c, v);
+    }
+    if (row0 < p.M) {
+      const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
+      const int e1 = b[1];
+      for (int e = b[0]; e < e1; ++e) {
+        const uint32_t rec = p.entry[e];
+        const int c = (rec >> 5) & 255;
+        if ((c >> 7) != half) continue;               // the same for the whole warp
+        const float y = tc_ld1(tacc + c);
+        if (ok && lane == (int)(rec & 31))             // this thread wrote the element above
+          d[c] = __bfloat16_as_ushort(__float2bfloat16_rn(
+              coef * (exp2_fast(fmaf(y, p.to_log2, -l)) - p.q[(int64_t)row * p.K + (rec >> 13)])));
+      }
+    }
+  } else {
+    const int64_t at = (int64_t)row * p.ldo + n0;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {               // N is a multiple of 32 here
+      tc_ld32(tacc + c, v);
+      if (!ok) continue;
+      if (p.add) {
+        const float4* a = reinterpret_cast<const float4*>(p.add + at + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 x = a[j];
+          v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
+        }
+      }
+      if (p.out32) {
+        float4* o = reinterpret_cast<float4*>(p.out32 + at + c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      if (p.out16) store_bf16x32(p.out16 + at + c, v);
+    }
+  }
+  if constexpr (EPI == HEAD_LSE) {
+    if (row0 < p.M) {
+      const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
+      const int e1 = b[1];
+      for (int e = b[0]; e < e1; ++e) {
+        const uint32_t rec = p.entry[e];
+        const int c = (rec >> 5) & 255;
+        if ((c >> 7) != half) continue;
+        const float y = tc_ld1(tacc + c);
+        if (ok && lane == (int)(rec & 31)) p.entry_logit[(int64_t)row * p.K + (rec >> 13)] = y;
+      }
+    }
+  }
+}
+
+// Tile w: bands of p.band row tiles; within a band the row tile varies fastest, so that the clusters at work share a
+// few tiles of A and of B, which stay in L2.
+__device__ __forceinline__ void head_tile(const HeadGemm& p, int w, int* mt, int* nt) {
+  const int per_band = p.band * p.tiles_n;
+  const int b = w / per_band, rem = w - b * per_band;
+  const int in_band = min(p.band, p.tiles_m - b * p.band);
+  *nt = rem / in_band;
+  *mt = b * p.band + (rem - *nt * in_band);
+}
+
+// A_MN / B_MN: the operand lies with its rows along K ([K][M] or [K][N] in memory).
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(HeadSmem::THREADS, 1)
+    head_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const HeadGemm p) {
+  using S = HeadSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S::STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S::STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S::STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * S::STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::BAR + 8 * (2 * S::STAGES + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * S::EPI_WARPS);   // both CTAs' epilogue warps
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&ta);
+    tma_prefetch_desc(&tb);
+  }
+  if (warp == 1) {
+    tc_alloc_pair(smem_u32(tmem_slot), S::TMEM_COLS);
+    tc_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();                                   // barriers and tensor memory are ready in both CTAs
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();                                       // no global memory access before this point
+
+  const int total = p.tiles_m * p.tiles_n;
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int w = cluster; w < total && ok; w += clusters) {
+        int mt, nt;
+        head_tile(p, w, &mt, &nt);
+        const int row = mt * 256 + 128 * (int)rank, col = nt * 256 + 128 * (int)rank;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, p.status, 701)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_expect_tx(full_bar(stage), 2 * S::STAGE);
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          const uint32_t sa = sbase + stage * S::STAGE, sb = sa + S::HALF;
+          const int k0 = kb * GEMM_BK;
+          if constexpr (A_MN) {
+            tma_load_2d_pair(sa, &ta, fb, row, k0);
+            tma_load_2d_pair(sa + 8192, &ta, fb, row + 64, k0);
+          } else {
+            tma_load_2d_pair(sa, &ta, fb, k0, row);
+          }
+          if constexpr (B_MN) {
+            tma_load_2d_pair(sb, &tb, fb, col, k0);
+            tma_load_2d_pair(sb + 8192, &tb, fb, col + 64, k0);
+          } else {
+            tma_load_2d_pair(sb, &tb, fb, k0, col);
+          }
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      pdl_trigger();                                // every load is issued: the next kernel may be scheduled
+      if (!ok) {
+        // A wait ran out: the copies in flight (this CTA's and the peer's) complete on the even CTA's barriers in an
+        // order that no longer says when the last one has landed, so both CTAs stay for far longer than a copy takes.
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 200000) {}
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs (even CTA)
+    if (leader) {
+      constexpr uint32_t idesc = instr_desc_bf16(256, 256, A_MN, B_MN);
+      int stage = 0, it = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int w = cluster; w < total && ok; w += clusters, ++it) {
+        const int acc = it & 1;
+        int good = 1;
+        if (lane == 0)
+          good = wait_bounded(tempty_bar(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.limit_ns, p.status, 702);
+        if (!__shfl_sync(0xffffffffu, good, 0)) break;
+        tc_fence_after();
+        const uint32_t tacc = tmem_base + acc * 256;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (lane == 0) good = wait_bounded(full_bar(stage), phase, abort_flag, p.limit_ns, p.status, 703);
+          if (!__shfl_sync(0xffffffffu, good, 0)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = sbase + stage * S::STAGE, sb = sa + S::HALF;
+          if (lane == 0) {
+#pragma unroll
+            for (int kk = 0; kk < GEMM_BK / 16; ++kk) {
+              const uint64_t ad = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024) : smem_desc_sw128(sa + kk * 32, 0, 1024);
+              const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 0, 1024);
+              tc_mma_pair(tacc, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+            }
+            tc_commit_pair(empty_bar(stage), 0x3);
+          }
+          __syncwarp();
+          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        if (lane == 0) tc_commit_pair(tfull_bar(acc), 0x3);
+        __syncwarp();
+      }
+      if (lane == 0) {                              // every MMA has completed before the tensor memory is freed
+        tc_commit_pair(drain_bar, 0x1);
+        volatile int no_abort = 0;
+        wait_bounded(drain_bar, 0, &no_abort, p.limit_ns, nullptr, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3, half = (warp - 2) >> 2;   // the quarter of the lanes this warp may read
+    int it = 0;
+    for (int w = cluster; w < total; w += clusters, ++it) {
+      const int acc = it & 1;
+      int good = 1;
+      if (lane == 0) good = wait_bounded(tfull_bar(acc), (it >> 1) & 1, abort_flag, p.limit_ns, p.status, 704);
+      if (!__shfl_sync(0xffffffffu, good, 0)) break;
+      tc_fence_after();
+      int mt, nt;
+      head_tile(p, w, &mt, &nt);
+      head_epilogue<EPI>(p, mt * 256 + 128 * (int)rank + q * 32, nt, half,
+                         tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256, lane);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(tempty_bar(acc));
+        else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();                                   // no CTA leaves while its peer may still signal it
+  tc_fence_after();
+  if (warp == 1) tc_dealloc_pair(tmem_base, S::TMEM_COLS);
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t launch_head_gemm(const CUtensorMap& a, const CUtensorMap& b, HeadGemm p, int sms, cudaStream_t s) {
+  auto kern = head_gemm_kernel<EPI, A_MN, B_MN>;
+  p.tiles_m = (p.M + 255) / 256;
+  p.tiles_n = (p.N + 255) / 256;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadSmem::TOTAL);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, sms / 2)));
+  cfg.blockDim = dim3(HeadSmem::THREADS);
+  cfg.dynamicSmemBytes = HeadSmem::TOTAL;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = launch_chain_mode() >= MOE_CHAIN_EARLY ? 2 : 1;   // the cluster attribute comes first
+  err = cudaLaunchKernelEx(&cfg, kern, a, b, p);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace moe
