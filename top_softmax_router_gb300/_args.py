@@ -1,19 +1,26 @@
 """Argument marshalling shared by the layer operators' bindings (norm.py, embed.py, scores.py, distill.py)."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}      # MOE_TYPE_* of moe_types.h
+_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream(device).cuda_stream without the Stream object
 INDEX_TYPES = {torch.int32: 0, torch.int64: 1}                       # MOE_INDEX_*
 
 
+def _is(dtype, wanted) -> bool:
+    return dtype in wanted if type(wanted) is dict else dtype is wanted
+
+
 def ptr(t, name: str, dtype, shape) -> int | None:
-    """Device pointer of a dense CUDA tensor of one of the types `dtype` and of `shape`; None stays None."""
+    """Device pointer of a dense CUDA tensor of `shape` and of type `dtype` (or one of a dict's); None stays None."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype not in dtype if isinstance(dtype, (dict, tuple)) else t.dtype != dtype:
+    if not _is(t.dtype, dtype):
         raise TypeError(f"{name}: unexpected type {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
@@ -28,7 +35,7 @@ def rows(t, name: str, dtype, shape) -> tuple[int, int]:
     """(device pointer, row stride) of a CUDA matrix whose rows are dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype not in dtype if isinstance(dtype, (dict, tuple)) else t.dtype != dtype:
+    if not _is(t.dtype, dtype):
         raise TypeError(f"{name}: unexpected type {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
@@ -62,7 +69,7 @@ class On:
     def __init__(self, stream, device):
         if stream is None:
             self.stream = None
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            self.handle = _raw_stream(device.index)
         else:
             self.stream = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
             self.handle = self.stream.cuda_stream
@@ -83,3 +90,18 @@ class On:
 def workspace(nbytes: int, device) -> torch.Tensor:
     """Zeroed, so that the status word starts clear."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+class Structs:
+    """A unit's C configuration by the number of rows of a call, as the pointer that the library takes."""
+
+    def __init__(self, cfg):
+        self._cfg, self._made = cfg, {}
+
+    def __call__(self, n: int):
+        got = self._made.get(n)
+        if got is None:
+            if len(self._made) >= 64:
+                self._made.clear()
+            got = self._made[n] = ctypes.pointer(self._cfg.c_struct(n))
+        return got

@@ -98,6 +98,8 @@ _lib = None
 
 def load() -> ctypes.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

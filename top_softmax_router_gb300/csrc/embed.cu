@@ -16,11 +16,12 @@
 namespace moe {
 namespace {
 
-constexpr int kPiece = 64;          // positions of a piece of a long run
-constexpr int kSortThreads = 512;   // 16 warps
+constexpr int kPiece = 64;           // positions of a piece of a long run
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kTile = 8192;         // positions sorted by one block
-constexpr int kMaxBits = 10;        // bits of a digit: kSortWarps x 1024 counters are 64 KB
+constexpr int kTile = 8192;          // most positions sorted by one block
+constexpr int kCluster = 8;          // blocks that sort together through distributed shared memory
+constexpr int kMaxBits = 9;          // bits of a digit: kSortWarps x 512 counters are 64 KB
 
 // ---------------------------------------------------------------------------
 // Forward: one warp a 16 x 32-byte piece of a row, so a short batch still spreads over the SMs.
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const I* __restrict__ id
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = c0 + (i * 32 + lane) * VEC;
-    if (c < H) p[i] = *reinterpret_cast<const Pack<T, VEC>*>(src + c);
+    if (c < H) p[i] = load_pack<T, VEC>(src + c);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -58,23 +59,17 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const I* __restrict__ id
       for (int j = 0; j < VEC; ++j) f[j] = ok ? f[j] * scale : 0.0f;
       p[i] = pack<T, VEC>(f);
     }
-    *reinterpret_cast<Pack<T, VEC>*>(dst + c) = p[i];
+    store_pack<T, VEC>(dst + c, p[i]);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Stable radix sort of (id, position)
 // ---------------------------------------------------------------------------
-// A block sorts a tile of kTile positions by one digit: warp w owns the tile's w-th consecutive
-// kTile / kSortWarps positions, 32 at a time; lanes with the same digit rank themselves by lane, so equal
-// digits keep their order.  cnt: [kSortWarps][bins] in shared memory, or the counters of a pass.
-template <class F>
-__device__ __forceinline__ void for_own_positions(int n, F&& f) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kOwn = kTile / kSortWarps;
-  const int end = min(n, (warp + 1) * kOwn);
-  for (int b = warp * kOwn; b < end; b += 32) f(b + lane, b + lane < end);   // the whole warp takes part
-}
+// A block sorts its positions by one digit: warp w owns the w-th consecutive `own` positions (a multiple of 32, at most
+// kTile / kSortWarps), 32 at a time; lanes with the same digit rank themselves by lane, so equal digits keep their
+// order.  cnt[w][d] counts them.
+constexpr int kSteps = kTile / kSortWarps / 32;
 
 // The key of a position: its id, or V (which sorts last) for one that adds to no gradient.
 template <class I>
@@ -87,34 +82,27 @@ __device__ __forceinline__ uint32_t token_key(const I* ids, int64_t n, int V, in
   return id == padding ? (uint32_t)V : (uint32_t)id;
 }
 
-// cnt[w][d] += positions of warp w with digit d.
-template <class K>
-__device__ __forceinline__ void count_digits(int* cnt, int bins, int n, K&& digit) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for_own_positions(n, [&](int i, bool in) {
-    const uint32_t d = in ? digit(i) : 0xFFFFFFFFu;
-    const uint32_t peers = __match_any_sync(0xffffffffu, d);
-    if (in && lane == __ffs(peers) - 1) cnt[warp * bins + d] += __popc(peers);
+// Counts the digits d[k] (of the warp's k-th 32 positions; 0xFFFFFFFF: no position) into the warp's counters, and
+// turns each d[k] into digit | rank << 16: how many of the warp's positions before it have the digit.
+__device__ __forceinline__ void rank_digits(int* cnt, uint32_t (&d)[kSteps]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const uint32_t peers = __match_any_sync(0xffffffffu, d[k]);
+    const bool in = d[k] != 0xFFFFFFFFu;
+    int before = 0;
+    if (in) before = cnt[d[k]] + __popc(peers & ((1u << lane) - 1u));
     __syncwarp();
-  });
+    if (in && lane == __ffs(peers) - 1) cnt[d[k]] += __popc(peers);
+    __syncwarp();
+    if (in) d[k] |= (uint32_t)before << 16;   // at most 256 of 512 digits: 9 + 9 bits
+  }
 }
 
-// Turns cnt[w][d] into the first place of warp w's digit d: the places of smaller digits, then those of the
-// same digit in earlier warps.  base(d): where digit d starts, given the tile's own count in front of it.
-template <class B>
-__device__ __forceinline__ void digit_places(int* cnt, int* scratch, int bins, B&& base) {
-  // thread t owns digits 2t and 2t + 1 (bins <= 1024)
-  int sum[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = threadIdx.x * 2 + k;
-    if (d < bins)
-      for (int w = 0; w < kSortWarps; ++w) sum[k] += cnt[w * bins + d];
-  }
-  // exclusive scan of the pairs over the block
+// Exclusive prefix sum over the block's threads.
+__device__ __forceinline__ int exclusive_scan(int v, int* scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = sum[0] + sum[1];
-  const int own = x;
+  int x = v;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, off);
@@ -122,74 +110,114 @@ __device__ __forceinline__ void digit_places(int* cnt, int* scratch, int bins, B
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  int before = x - own;
-  for (int w = 0; w < warp; ++w) before += scratch[w];
+  int w = lane < warp ? scratch[lane] : 0;   // 32 warps
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = threadIdx.x * 2 + k;
-    if (d < bins) {
-      int at = base(d, before);
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = cnt[w * bins + d];
-        cnt[w * bins + d] = at;
-        at += c;
-      }
+  for (int off = 16; off > 0; off >>= 1) w += __shfl_xor_sync(0xffffffffu, w, off);
+  return w + x - v;
+}
+
+// cnt[w][d] becomes the first place of warp w's digit d, where the block's digit d starts at `start` (of thread d).
+__device__ __forceinline__ void warp_places(int* cnt, int bins, int start) {
+  const int d = threadIdx.x;
+  if (d < bins) {
+    int at = start;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = cnt[w * bins + d];
+      cnt[w * bins + d] = at;
+      at += c;
     }
-    before += sum[k];
   }
-  __syncthreads();
+}
+__device__ __forceinline__ int digit_total(const int* cnt, int bins) {
+  int s = 0;
+  const int d = threadIdx.x;
+  if (d < bins)
+    for (int w = 0; w < kSortWarps; ++w) s += cnt[w * bins + d];
+  return s;
 }
 
-// Hands each position of the tile its place: put(i, place).
-template <class K, class F>
-__device__ __forceinline__ void place_all(int* cnt, int bins, int n, K&& digit, F&& put) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for_own_positions(n, [&](int i, bool in) {
-    const uint32_t d = in ? digit(i) : 0xFFFFFFFFu;
-    const uint32_t peers = __match_any_sync(0xffffffffu, d);
-    int at = 0;
-    if (in) at = cnt[warp * bins + d] + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();
-    if (in && lane == __ffs(peers) - 1) cnt[warp * bins + d] += __popc(peers);
-    __syncwarp();
-    if (in) put(i, at);
-  });
+__device__ __forceinline__ uint32_t cluster_blocks() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int load_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// N <= kTile: all passes in one block.  Keys and positions stay in shared memory between passes.
+// N <= kCluster x kTile: one launch of one cluster.  Block c holds places [c cap, (c + 1) cap) as (key, position) pairs
+// in shared memory; a pass counts its digits, reads the other blocks' counts, and stores each pair into the block of
+// its new place.  The cluster's barrier separates the passes.  (As two launches a pass over global memory the same
+// sort of 32768 tokens took 75 us.)
 template <class I>
 __global__ void __launch_bounds__(kSortThreads, 1)
-    embed_sort_one_kernel(const I* __restrict__ ids, uint32_t* __restrict__ keys, int* __restrict__ order, int N, int V,
-                          int padding, int passes, int bits, int* status) {
+    embed_sort_cluster_kernel(const I* __restrict__ ids, uint32_t* __restrict__ keys, int* __restrict__ order, int N,
+                              int V, int padding, int cap, int passes, int bits, int* status) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ uint32_t sm[];
-  uint32_t* key[2] = {sm, sm + 2 * kTile};            // key[p][i], position key[p][kTile + i]
-  int* cnt = reinterpret_cast<int*>(sm + 4 * kTile);
-  __shared__ int scratch[32];
+  extern __shared__ __align__(16) uint32_t sm[];
   const int bins = 1 << bits;
-  for (int i = threadIdx.x; i < N; i += kSortThreads) {
-    key[0][i] = token_key(ids, i, V, padding, status);
-    key[0][kTile + i] = i;
-  }
+  uint2* buf[2] = {reinterpret_cast<uint2*>(sm), reinterpret_cast<uint2*>(sm) + cap};
+  int* cnt = reinterpret_cast<int*>(sm + 4 * cap);      // [kSortWarps][bins]
+  int* total = cnt + kSortWarps * bins;                 // [bins], read by the other blocks
+  __shared__ int scratch[32];
+  const int rank = (int)cluster_ctarank(), blocks = (int)cluster_blocks();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = max(0, min(cap, N - rank * cap));    // places this block holds
+  const int own = (cap / kSortWarps + 31) / 32 * 32, first = warp * own;
+  const uint32_t total_addr = smem_u32(total);
   for (int p = 0; p < passes; ++p) {
-    uint32_t *in = key[p & 1], *out = key[(p & 1) ^ 1];
+    uint2* in = buf[p & 1];
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
-    auto digit = [&](int i) { return (in[i] >> (p * bits)) & (bins - 1u); };
-    count_digits(cnt, bins, N, digit);
+    uint2 pair[kSteps];
+    uint32_t d[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int i = first + k * 32 + lane;
+      d[k] = 0xFFFFFFFFu;
+      if (k * 32 < own && i < mine) {
+        pair[k] = p == 0 ? make_uint2(token_key(ids, rank * cap + i, V, padding, status), (uint32_t)(rank * cap + i)) : in[i];
+        d[k] = (pair[k].x >> (p * bits)) & (bins - 1u);
+      }
+    }
+    rank_digits(cnt + warp * bins, d);
     __syncthreads();
-    digit_places(cnt, scratch, bins, [](int, int before) { return before; });
-    place_all(cnt, bins, N, digit, [&](int i, int at) {
-      out[at] = in[i];
-      out[kTile + at] = in[kTile + i];
-    });
+    const int sum = digit_total(cnt, bins);
+    if ((int)threadIdx.x < bins) total[threadIdx.x] = sum;
+    __syncwarp();
+    cluster_sync();
+    int all = 0, ahead = 0;
+    if ((int)threadIdx.x < bins)
+      for (int c = 0; c < blocks; ++c) {
+        const int v = load_cluster(mapa_shared(total_addr + 4 * threadIdx.x, c));
+        all += v;
+        if (c < rank) ahead += v;
+      }
+    const int before = exclusive_scan(all, scratch);
+    warp_places(cnt, bins, before + ahead);
     __syncthreads();
-  }
-  const uint32_t* done = key[passes & 1];
-  for (int i = threadIdx.x; i < N; i += kSortThreads) {
-    keys[i] = done[i];
-    order[i] = (int)done[kTile + i];
+    const bool last = p + 1 == passes;
+    const uint32_t out = smem_u32(buf[(p & 1) ^ 1]);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      if (d[k] == 0xFFFFFFFFu) continue;
+      const int at = cnt[warp * bins + (d[k] & 0xFFFFu)] + (int)(d[k] >> 16);
+      if (last) {
+        keys[at] = pair[k].x;
+        order[at] = (int)pair[k].y;
+      } else {
+        const int c = at / cap;
+        store_cluster(mapa_shared(out + 8 * (at - c * cap), c), pair[k].x, pair[k].y);
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // every pair is in place, and nobody still reads this pass's totals
   }
 }
 
@@ -206,29 +234,24 @@ struct SortIn {
   __device__ __forceinline__ int position(int64_t i) const { return ids ? (int)i : order[i]; }
 };
 
-// Digit counts of each tile: counts[tile][digit].
+// More tokens: digit counts of each tile of kTile positions, counts[tile][digit], ..
 template <class I>
 __global__ void __launch_bounds__(kSortThreads, 1)
     embed_count_kernel(SortIn<I> in, int* __restrict__ counts, int N, int shift, int bits, int* status) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ uint32_t sm[];
-  int* cnt = reinterpret_cast<int*>(sm);
+  __shared__ int cnt[1 << kMaxBits];
   const int bins = 1 << bits;
-  for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+  if ((int)threadIdx.x < bins) cnt[threadIdx.x] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * kTile;
   const int n = (int)min((int64_t)kTile, N - t0);
-  count_digits(cnt, bins, n, [&](int i) { return (in.key(t0 + i, status) >> shift) & (bins - 1u); });
+  for (int i = threadIdx.x; i < n; i += kSortThreads) atomicAdd(cnt + ((in.key(t0 + i, status) >> shift) & (bins - 1u)), 1);
   __syncthreads();
-  for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-    int s = 0;
-    for (int w = 0; w < kSortWarps; ++w) s += cnt[w * bins + d];
-    counts[(int64_t)blockIdx.x * bins + d] = s;
-  }
+  if ((int)threadIdx.x < bins) counts[(int64_t)blockIdx.x * bins + threadIdx.x] = cnt[threadIdx.x];
 }
 
-// Each tile finds the places of its digits from all tiles' counts (smaller digits of every tile, then the same
+// .. then each tile finds the places of its digits from all tiles' counts (smaller digits of every tile, then the same
 // digit of earlier tiles) and scatters its pairs.
 template <class I>
 __global__ void __launch_bounds__(kSortThreads, 1)
@@ -236,61 +259,51 @@ __global__ void __launch_bounds__(kSortThreads, 1)
                          int* __restrict__ order, int N, int shift, int bits) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(16) uint32_t sm[];
   const int bins = 1 << bits;
   int* cnt = reinterpret_cast<int*>(sm);
-  int* start = cnt + kSortWarps * bins;     // this tile's first place of each digit
-  __shared__ int scratch[32], total_before[32];
-  const int tiles = gridDim.x, mine = blockIdx.x;
-  for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
-  // start[d] = sum over d' < d of all tiles' counts + sum over earlier tiles of counts[d]
-  int sum[2] = {0, 0}, ahead[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = threadIdx.x * 2 + k;
-    if (d < bins)
-      for (int t = 0; t < tiles; ++t) {
-        const int c = counts[(int64_t)t * bins + d];
-        sum[k] += c;
-        if (t < mine) ahead[k] += c;
-      }
-  }
+  __shared__ int scratch[32];
+  const int tiles = gridDim.x, tile = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = sum[0] + sum[1];
-  const int own = x;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
-  }
-  if (lane == 31) total_before[warp] = x;
-  __syncthreads();
-  int before = x - own;
-  for (int w = 0; w < warp; ++w) before += total_before[w];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = threadIdx.x * 2 + k;
-    if (d < bins) start[d] = before + ahead[k];
-    before += sum[k];
-  }
-  __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * kTile;
+  for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+  const int64_t t0 = (int64_t)tile * kTile;
   const int n = (int)min((int64_t)kTile, N - t0);
-  // (the counting kernel has reported bad ids)
-  auto digit = [&](int i) { return (in.key(t0 + i, nullptr) >> shift) & (bins - 1u); };
-  count_digits(cnt, bins, n, digit);
+  uint32_t key[kSteps], d[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int i = warp * (kTile / kSortWarps) + k * 32 + lane;
+    d[k] = 0xFFFFFFFFu;
+    if (i < n) {
+      key[k] = in.key(t0 + i, nullptr);   // the counting kernel has reported bad ids
+      d[k] = (key[k] >> shift) & (bins - 1u);
+    }
+  }
+  int all = 0, ahead = 0;
+  if ((int)threadIdx.x < bins)
+    for (int t = 0; t < tiles; ++t) {
+      const int c = counts[(int64_t)t * bins + threadIdx.x];
+      all += c;
+      if (t < tile) ahead += c;
+    }
   __syncthreads();
-  digit_places(cnt, scratch, bins, [&](int d, int) { return start[d]; });
-  place_all(cnt, bins, n, digit, [&](int i, int at) {
-    keys[at] = in.key(t0 + i, nullptr);
-    order[at] = in.position(t0 + i);
-  });
+  rank_digits(cnt + warp * bins, d);
+  __syncthreads();
+  const int before = exclusive_scan(all, scratch);
+  warp_places(cnt, bins, before + ahead);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    if (d[k] == 0xFFFFFFFFu) continue;
+    const int at = cnt[warp * bins + (d[k] & 0xFFFFu)] + (int)(d[k] >> 16);
+    keys[at] = key[k];
+    order[at] = in.position(t0 + warp * (kTile / kSortWarps) + k * 32 + lane);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Sums over the runs
 // ---------------------------------------------------------------------------
-// First index in [lo, hi) of the ascending keys whose key is >= v.
+// First index in [lo, hi) of the ascending keys whose key is >= v (hi if there is none).
 __device__ __forceinline__ int lower_bound(const uint32_t* keys, int lo, int hi, uint32_t v) {
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -300,17 +313,34 @@ __device__ __forceinline__ int lower_bound(const uint32_t* keys, int lo, int hi,
   return lo;
 }
 
-// a[j] += sum over sorted places [s, e) of dy[order[place]][c + j], in order, four rows' loads at a time.
+// The same over [0, n) by a whole warp: 32 probes a step, three steps for 32768 keys.
+__device__ __forceinline__ int lower_bound_warp(const uint32_t* keys, int n, uint32_t v) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;   // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5;
+    const int at = lo + lane * step;
+    const uint32_t less = __ballot_sync(0xffffffffu, at < hi && keys[at] < v);
+    if (!less) return lo;
+    const int k = 31 - __clz(less);        // probes 0 .. k are below v
+    const int next = lo + (k + 1) * step;
+    lo = lo + k * step + 1;
+    hi = min(hi, next);
+  }
+  return lo;
+}
+
+// a[j] += sum over sorted places [s, e) of dy[order[place]][c + j], in order, eight rows' loads at a time.
 template <class T, int VEC>
 __device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy, const int* __restrict__ order, int s,
                                          int e, int c, float (&a)[VEC]) {
   int i = s;
-  for (; i + 4 <= e; i += 4) {
-    Pack<T, VEC> p[4];
+  for (; i + 8 <= e; i += 8) {
+    Pack<T, VEC> p[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) p[k] = *reinterpret_cast<const Pack<T, VEC>*>(dy + order[i + k] * lddy + c);
+    for (int k = 0; k < 8; ++k) p[k] = load_pack<T, VEC>(dy + order[i + k] * lddy + c);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       float f[VEC];
       unpack<T, VEC>(p[k], f);
 #pragma unroll
@@ -318,7 +348,7 @@ __device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy,
     }
   }
   for (; i < e; ++i) {
-    const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC>*>(dy + order[i] * lddy + c);
+    const Pack<T, VEC> p = load_pack<T, VEC>(dy + order[i] * lddy + c);
     float f[VEC];
     unpack<T, VEC>(p, f);
 #pragma unroll
@@ -337,9 +367,11 @@ __global__ void __launch_bounds__(256) embed_piece_kernel(const uint32_t* __rest
   pdl_trigger();
   __shared__ int edge[4];   // run of the first place: start, end; run of the last place: start, end
   const int p0 = blockIdx.x * kPiece, p1 = min(N, p0 + kPiece);
-  if (threadIdx.x < 4) {
-    const uint32_t v = keys[threadIdx.x < 2 ? p0 : p1 - 1];
-    edge[threadIdx.x] = v >= (uint32_t)V ? 0 : lower_bound(keys, 0, N, v + (threadIdx.x & 1));
+  const int warp = threadIdx.x >> 5;
+  if (warp < 4) {
+    const uint32_t v = keys[warp < 2 ? p0 : p1 - 1];
+    const int at = v >= (uint32_t)V ? 0 : lower_bound_warp(keys, N, v + (warp & 1));
+    if ((threadIdx.x & 31) == 0) edge[warp] = at;
   }
   __syncthreads();
   const int s0 = edge[0], e0 = edge[1], s1 = edge[2], e1 = edge[3];
@@ -350,62 +382,73 @@ __global__ void __launch_bounds__(256) embed_piece_kernel(const uint32_t* __rest
     float* out = part + ((int64_t)blockIdx.x * 2 + which) * H;
     for (int c = (blockIdx.y * 256 + threadIdx.x) * VEC; c < H; c += gridDim.y * 256 * VEC) {
       float a[VEC];
+      Pack<float, VEC> o;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) a[j] = 0.0f;
       add_rows<T, VEC>(dy, lddy, order, a0, a1, c, a);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) out[c + j] = a[j];
+      for (int j = 0; j < VEC; ++j) o.v[j] = a[j];
+      store_pack<float, VEC>(out + c, o);
     }
   }
 }
 
-// Block b owns table rows [R b, R (b + 1)); its threads walk over (row, pack of columns).
+// Block b owns table rows [R b, R (b + 1)), `tpr` threads (a power of two) a row; thread t of a row takes the packs
+// t, t + tpr, ..  Four floats a pack: a warp's store is one run of 512 bytes.
 template <class T, int VEC, bool ADD>
 __global__ void __launch_bounds__(256) embed_rows_kernel(const uint32_t* __restrict__ keys,
                                                         const int* __restrict__ order, const T* __restrict__ dy,
                                                         int64_t lddy, const float* __restrict__ part,
-                                                        float* __restrict__ dW, int N, int V, int H, int R,
+                                                        float* __restrict__ dW, int N, int V, int H, int R, int tpr,
                                                         float scale) {
   pdl_wait();
   pdl_trigger();
   __shared__ int first[257];   // first[r]: first place of row v0 + r; R <= 256
   const int64_t v0 = (int64_t)blockIdx.x * R;
   const int rows = (int)min((int64_t)R, V - v0);
-  if (threadIdx.x < 2) first[threadIdx.x ? rows : 0] = lower_bound(keys, 0, N, (uint32_t)(v0 + (threadIdx.x ? rows : 0)));
+  if (threadIdx.x < 64) {
+    const int r = threadIdx.x < 32 ? 0 : rows;
+    const int at = lower_bound_warp(keys, N, (uint32_t)(v0 + r));
+    if ((threadIdx.x & 31) == 0) first[r] = at;
+  }
   __syncthreads();
   const int lo = first[0], hi = first[rows];
   if (ADD && lo == hi) return;
   if (threadIdx.x > 0 && (int)threadIdx.x < rows) first[threadIdx.x] = lower_bound(keys, lo, hi, (uint32_t)(v0 + threadIdx.x));
   __syncthreads();
-  const int packs = H / VEC;
-  for (int u = threadIdx.x; u < rows * packs; u += 256) {
-    const int r = u / packs, c = (u - r * packs) * VEC;
+  const int t = threadIdx.x & (tpr - 1);
+  for (int r = threadIdx.x / tpr; r < rows; r += 256 / tpr) {
     const int s = first[r], e = first[r + 1];
     if (ADD && s == e) continue;
-    float a[VEC];
+    float* row = dW + (v0 + r) * H;
+    for (int c = t * VEC; c < H; c += tpr * VEC) {
+      Pack<float, VEC> o;
+      float a[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) a[j] = 0.0f;
-    if (e - s <= kPiece) {
-      add_rows<T, VEC>(dy, lddy, order, s, e, c, a);
-    } else {
-      for (int b = s / kPiece; b <= (e - 1) / kPiece; ++b) {
-        const float* p = part + ((int64_t)b * 2 + (b * kPiece < s ? 1 : 0)) * H + c;
+      for (int j = 0; j < VEC; ++j) a[j] = 0.0f;
+      if (e - s <= kPiece) {
+        add_rows<T, VEC>(dy, lddy, order, s, e, c, a);
+      } else {
+        for (int b = s / kPiece; b <= (e - 1) / kPiece; ++b) {
+          const Pack<float, VEC> p = load_pack<float, VEC>(part + ((int64_t)b * 2 + (b * kPiece < s ? 1 : 0)) * H + c);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) a[j] += p[j];
+          for (int j = 0; j < VEC; ++j) a[j] += p.v[j];
+        }
+      }
+      if (ADD) {
+        o = load_pack<float, VEC>(row + c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o.v[j] = fmaf(scale, a[j], o.v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o.v[j] = scale * a[j];
+      }
+      if constexpr (VEC == 4) {   // written once and not read again here: first to leave L2
+        __stcs(reinterpret_cast<float4*>(row + c), make_float4(o.v[0], o.v[1], o.v[2], o.v[3]));
+      } else {
+        store_pack<float, VEC>(row + c, o);
       }
     }
-    float* out = dW + (v0 + r) * H + c;
-    using Out = Pack<float, VEC>;
-    Out o;
-    if (ADD) {
-      o = *reinterpret_cast<const Out*>(out);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o.v[j] = fmaf(scale, a[j], o.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o.v[j] = scale * a[j];
-    }
-    *reinterpret_cast<Out*>(out) = o;
   }
 }
 
@@ -466,21 +509,39 @@ cudaError_t sort_tokens(const moe_embed_config& c, const EmbedLayout& L, const I
   auto keys = [&](int i) { return reinterpret_cast<uint32_t*>(w + L.keys[i]); };
   auto order = [&](int i) { return reinterpret_cast<int*>(w + L.order[i]); };
   const size_t cnt = (size_t)kSortWarps * (1u << L.bits) * 4;
-  if (L.tiles == 1) {
-    const size_t smem = (size_t)4 * kTile * 4 + cnt;   // at most 192 KB
-    const cudaError_t e = allow_smem(embed_sort_one_kernel<I>, smem);
+  if (c.N <= kCluster * kTile) {
+    // a block for each 2048 tokens, up to the cluster's 8; `cap` a multiple of the warps' steps
+    int blocks = 1;
+    while (blocks < kCluster && c.N > blocks * 2048) blocks *= 2;
+    const int cap = ((c.N + blocks - 1) / blocks + 1023) / 1024 * 1024;
+    const size_t smem = (size_t)cap * 16 + cnt + (size_t)(1u << L.bits) * 4;   // at most 194 KB
+    auto kern = embed_sort_cluster_kernel<I>;
+    cudaError_t e = allow_smem(kern, smem);
     if (e != cudaSuccess) return e;
     *at = 0;
-    return launch_pdl(embed_sort_one_kernel<I>, dim3(1), dim3(kSortThreads), smem, s, ids, keys(0), order(0), c.N, c.V,
-                      c.padding_idx, L.passes, L.bits, status);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = launch_chain_mode() >= MOE_CHAIN_EARLY ? 2 : 1;   // the cluster attribute comes first
+    e = cudaLaunchKernelEx(&cfg, kern, ids, keys(0), order(0), c.N, c.V, c.padding_idx, cap, L.passes, L.bits, status);
+    return e != cudaSuccess ? e : cudaGetLastError();
   }
-  const size_t smem = cnt + (size_t)(1u << L.bits) * 4;
-  cudaError_t e = allow_smem(embed_count_kernel<I>, smem);
-  if (e == cudaSuccess) e = allow_smem(embed_scatter_kernel<I>, smem);
+  const size_t smem = cnt;
+  cudaError_t e = allow_smem(embed_scatter_kernel<I>, smem);
   int* counts = reinterpret_cast<int*>(w + L.counts);
   for (int p = 0; p < L.passes && e == cudaSuccess; ++p) {
     SortIn<I> in = {p == 0 ? ids : nullptr, keys((p + 1) & 1), order((p + 1) & 1), c.V, c.padding_idx};
-    e = launch_pdl(embed_count_kernel<I>, dim3(L.tiles), dim3(kSortThreads), smem, s, in, counts, c.N, p * L.bits,
+    e = launch_pdl(embed_count_kernel<I>, dim3(L.tiles), dim3(kSortThreads), 0, s, in, counts, c.N, p * L.bits,
                    L.bits, status);
     if (e == cudaSuccess)
       e = launch_pdl(embed_scatter_kernel<I>, dim3(L.tiles), dim3(kSortThreads), smem, s, in,
@@ -580,18 +641,19 @@ int moe_embed_backward(const moe_embed_config* cfg, const void* ids, int32_t id_
                                            part, c.N, c.V, c.H);
           if (e != cudaSuccess) return e;
         }
-        // rows a block: about 64 KB of gradient, so that the two searches of a block are paid for
-        const int R = (int)std::min<int64_t>(256, std::max<int64_t>(1, 16384 / c.H));
+        // rows a block: about 128 KB of gradient, so that the two searches of a block are paid for
+        const int R = (int)std::min<int64_t>(256, std::max<int64_t>(1, 32768 / c.H));
         const dim3 grid((unsigned)(((int64_t)c.V + R - 1) / R));
+        int tpr = 1;
+        while (tpr < 256 && tpr * VEC < c.H) tpr *= 2;
         if (accumulate)
           return launch_pdl(embed_rows_kernel<T, VEC, true>, grid, dim3(256), 0, s, keys, order, g, lddy,
-                            static_cast<const float*>(part), dW, c.N, c.V, c.H, R, c.scale);
+                            static_cast<const float*>(part), dW, c.N, c.V, c.H, R, tpr, c.scale);
         return launch_pdl(embed_rows_kernel<T, VEC, false>, grid, dim3(256), 0, s, keys, order, g, lddy,
-                          static_cast<const float*>(part), dW, c.N, c.V, c.H, R, c.scale);
+                          static_cast<const float*>(part), dW, c.N, c.V, c.H, R, tpr, c.scale);
       };
-      constexpr int V16 = 16 / sizeof(T);
-      if (c.H % V16 == 0 && lddy % V16 == 0 && aligned_to(dy, 16) && aligned_to(dW, 16))
-        return go(std::integral_constant<int, V16>{});
+      if (c.H % 4 == 0 && lddy % 4 == 0 && aligned_to(dy, 4 * ts) && aligned_to(dW, 16))
+        return go(std::integral_constant<int, 4>{});
       return go(std::integral_constant<int, 1>{});
     });
   });

@@ -12,9 +12,8 @@
 namespace moe {
 namespace {
 
-// A row is held in registers by `tpr` threads (32, or a multiple of 128), PER packs of VEC elements each:
-// pack i of thread t holds columns VEC (t + i tpr) ..  A block of max(tpr, 128) threads holds
-// block / tpr rows at a time.
+// A row is held in registers by `tpr` threads (a multiple of 32), PER packs of VEC elements each: pack i of
+// thread t holds columns VEC (t + i tpr) ..  A block holds block / tpr rows at a time.
 struct RowShape {
   int tpr, block, rows;   // threads per row, threads per block, rows per block
 };
@@ -33,76 +32,73 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* re
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-// One pass: x is read once, kept in registers for the mean, the variance around it and the output.
-template <class T, class P, int VEC, int PER, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) norm_fwd_kernel(const T* __restrict__ x, int64_t ldx,
-                                                       const P* __restrict__ weight, const P* __restrict__ bias,
-                                                       T* __restrict__ y, float* __restrict__ mean,
-                                                       float* __restrict__ rstd, int N, int H, float eps, int tpr) {
+// One pass: x is read once, kept in registers for the mean, the variance around it and the output.  TPR threads a row
+// at compile time, so that the packs' addresses are constants from the thread's first; places past the row hold zeros
+// and are masked by data, not by branches (with both at run time the arithmetic of 32768 x 7168 held it at 195 us).
+template <class T, class P, int VEC, int PER, int TPR, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+    norm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__ weight, const P* __restrict__ bias,
+                    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, int N, int H, float eps) {
   pdl_wait();
   pdl_trigger();
+  constexpr int PAIRS = pairs_of<VEC>;
   __shared__ float2 red[2][32];
-  const int t = threadIdx.x % tpr;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-  const int packs = H / VEC;
-  const bool row_ok = row < N;
-  const T* xr = x + row * ldx;
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+  if (row >= N) return;   // only where a row is a warp's own
+  const int left = H / VEC - t;   // pack i of the thread is in the row where i TPR < left
+  const T* xr = x + row * ldx + t * VEC;
   Pack<T, VEC> raw[PER];
-  float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = t + i * tpr;
-    if (row_ok && c < packs) raw[i] = *reinterpret_cast<const Pack<T, VEC>*>(xr + (int64_t)c * VEC);
+    raw[i] = zero_pack<T, VEC>();
+    if (i * TPR < left) raw[i] = load_pack<T, VEC>(xr + i * TPR * VEC);
   }
+  f32x2 s2(0.0f);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (row_ok && t + i * tpr < packs) {
-      float f[VEC];
-      unpack<T, VEC>(raw[i], f);
+    f32x2 f[PAIRS];
+    unpack2<T, VEC>(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) s += f[j];
-    }
+    for (int j = 0; j < PAIRS; ++j) s2 = add2(s2, f[j]);
   }
   const float inv_h = 1.0f / (float)H;
-  const float mu = row_sum2(s, 0.0f, tpr, red[0]).x * inv_h;
-  float q = 0.0f;
+  const float mu = row_sum2(s2.sum(), 0.0f, TPR, red[0]).x * inv_h;
+  f32x2 q2(0.0f);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (row_ok && t + i * tpr < packs) {
-      float f[VEC];
-      unpack<T, VEC>(raw[i], f);
+    const f32x2 minus_mu(i * TPR < left ? -mu : 0.0f, VEC > 1 && i * TPR < left ? -mu : 0.0f);
+    f32x2 f[PAIRS];
+    unpack2<T, VEC>(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) q = fmaf(f[j] - mu, f[j] - mu, q);
+    for (int j = 0; j < PAIRS; ++j) {
+      const f32x2 d = add2(f[j], minus_mu);
+      q2 = fma2(d, d, q2);
     }
   }
-  const float rs = 1.0f / sqrtf(row_sum2(q, 0.0f, tpr, red[1]).x * inv_h + eps);
-  if (!row_ok) return;
+  const float rs = 1.0f / sqrtf(row_sum2(q2.sum(), 0.0f, TPR, red[1]).x * inv_h + eps);
   if (t == 0) {
     if (mean) mean[row] = mu;
     if (rstd) rstd[row] = rs;
   }
+  const f32x2 rs2(rs), minus_mu(-mu);
+  T* yr = y + row * H + t * VEC;
+  const P* wt = weight + t * VEC;
+  const P* bt = bias + t * VEC;
+  const bool has_w = weight != nullptr, has_b = bias != nullptr;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = t + i * tpr;
-    if (c < packs) {
-      float f[VEC], o[VEC];
-      unpack<T, VEC>(raw[i], f);
+    const bool in = i * TPR < left;
+    f32x2 f[PAIRS], w[PAIRS], b[PAIRS];
+    Pack<P, VEC> pw = one_pack<P, VEC>(), pb = zero_pack<P, VEC>();
+    if (in && has_w) pw = load_pack<P, VEC>(wt + i * TPR * VEC);
+    if (in && has_b) pb = load_pack<P, VEC>(bt + i * TPR * VEC);
+    unpack2<T, VEC>(raw[i], f);
+    unpack2<P, VEC>(pw, w);
+    unpack2<P, VEC>(pb, b);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o[j] = (f[j] - mu) * rs;
-      if (weight) {
-        Pack<P, VEC> w = *reinterpret_cast<const Pack<P, VEC>*>(weight + c * VEC);
-        unpack<P, VEC>(w, f);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] *= f[j];
-      }
-      if (bias) {
-        Pack<P, VEC> b = *reinterpret_cast<const Pack<P, VEC>*>(bias + c * VEC);
-        unpack<P, VEC>(b, f);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] += f[j];
-      }
-      *reinterpret_cast<Pack<T, VEC>*>(y + row * H + (int64_t)c * VEC) = pack<T, VEC>(o);
-    }
+    for (int j = 0; j < PAIRS; ++j) f[j] = fma2(mul2(add2(f[j], minus_mu), rs2), w[j], b[j]);
+    if (in) store_pack<T, VEC>(yr + i * TPR * VEC, pack2<T, VEC>(f));
   }
 }
 
@@ -128,19 +124,30 @@ __global__ void __launch_bounds__(THREADS, 1) norm_bwd_kernel(const T* __restric
 #pragma unroll
     for (int j = 0; j < VEC; ++j) gw[i][j] = gb[i][j] = 0.0f;
   int it = 0;
+  Pack<T, VEC> nx[PER], nd[PER];   // the next row, loaded while this one is worked on
+  float mu_next = 0.0f, rs_next = 0.0f;
+  auto load = [&](int64_t row) {
+    if (row >= N) return;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = t + i * tpr;
+      if (c < packs) {
+        nx[i] = load_pack<T, VEC>(x + row * ldx + (int64_t)c * VEC);
+        nd[i] = load_pack<T, VEC>(dy + row * lddy + (int64_t)c * VEC);
+      }
+    }
+    mu_next = mean[row];
+    rs_next = rstd[row];
+  };
+  load((int64_t)blockIdx.x * rpb + sub);
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < N; base += (int64_t)gridDim.x * rpb, ++it) {
     const int64_t row = base + sub;
     const bool row_ok = row < N;
     Pack<T, VEC> rx[PER], rd[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = t + i * tpr;
-      if (row_ok && c < packs) {
-        rx[i] = *reinterpret_cast<const Pack<T, VEC>*>(x + row * ldx + (int64_t)c * VEC);
-        rd[i] = *reinterpret_cast<const Pack<T, VEC>*>(dy + row * lddy + (int64_t)c * VEC);
-      }
-    }
-    const float mu = row_ok ? mean[row] : 0.0f, rs = row_ok ? rstd[row] : 0.0f;
+    for (int i = 0; i < PER; ++i) rx[i] = nx[i], rd[i] = nd[i];
+    const float mu = mu_next, rs = rs_next;
+    load(row + (int64_t)gridDim.x * rpb);
     float s = 0.0f, sx = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_bwd_kernel(const T* __restric
         unpack<T, VEC>(rx[i], fx);
         unpack<T, VEC>(rd[i], fd);
         if (weight) {
-          Pack<P, VEC> w = *reinterpret_cast<const Pack<P, VEC>*>(weight + c * VEC);
+          Pack<P, VEC> w = load_pack<P, VEC>(weight + c * VEC);
           unpack<P, VEC>(w, fw);
         }
 #pragma unroll
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_bwd_kernel(const T* __restric
           unpack<T, VEC>(rx[i], fx);
           unpack<T, VEC>(rd[i], fd);
           if (weight) {
-            Pack<P, VEC> w = *reinterpret_cast<const Pack<P, VEC>*>(weight + c * VEC);
+            Pack<P, VEC> w = load_pack<P, VEC>(weight + c * VEC);
             unpack<P, VEC>(w, fw);
           }
 #pragma unroll
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_bwd_kernel(const T* __restric
             const float tj = weight ? fd[j] * fw[j] : fd[j];
             o[j] = rs * (tj - a - xh * b);
           }
-          *reinterpret_cast<Pack<T, VEC>*>(dx + row * H + (int64_t)c * VEC) = pack<T, VEC>(o);
+          store_pack<T, VEC>(dx + row * H + (int64_t)c * VEC, pack<T, VEC>(o));
         }
       }
     }
@@ -210,6 +217,209 @@ __global__ void __launch_bounds__(THREADS, 1) norm_bwd_kernel(const T* __restric
       }
     }
     if (r + 1 < rpb) __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Wide rows: a ring of rows in shared memory
+// ---------------------------------------------------------------------------
+// The last warp of a block streams the block's rows of x and dy into `stages` places of shared memory with bulk
+// copies; the other threads (`workers`) hold up to four packs of columns each and meet once a row for its
+// sums.  The copies run ahead of the reductions, so the memory stays busy, and the blocks that share an SM work while
+// the others meet.  The weight lies in shared memory in fp32.  A thread whose last packs are past the row reads
+// the row's last pack in their place and adds nothing, so that the arithmetic has no branches.
+constexpr int kRingMost = 8;
+constexpr int kRingSm = 228 * 1024;            // shared memory of an SM, of which a block costs 1 KB and its own variables
+constexpr int kRingFixed = 2 * kRingMost * 8;  // full[kRingMost], empty[kRingMost]
+
+// One contiguous copy of global memory into shared memory, completing on `bar` (16-byte multiples).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+struct Ring {
+  uint32_t base, bars;
+  int stages, stage_bytes;
+  volatile int* abort_flag;
+  int64_t limit_ns;
+  int* status;
+  __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
+  __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (kRingMost + s); }
+  // Rows blockIdx.x, + gridDim.x, ..: one thread.
+  __device__ __forceinline__ void stream(const void* a, int64_t lda, const void* b, int64_t ldb, int row_bytes, int N) const {
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < N; row += gridDim.x) {
+      if (!wait_bounded(empty(stage), phase ^ 1u, abort_flag, limit_ns, status, 801)) break;
+      const uint32_t dst = base + stage * stage_bytes;
+      mbar_expect_tx(full(stage), stage_bytes);
+      bulk_load(dst, static_cast<const uint8_t*>(a) + row * lda, row_bytes, full(stage));
+      if (b) bulk_load(dst + row_bytes, static_cast<const uint8_t*>(b) + row * ldb, row_bytes, full(stage));
+      ++issued;
+      if (++stage == stages) stage = 0, phase ^= 1u;
+    }
+    // every copy has landed before the block leaves, also after a wait that ran out
+    for (int q = 1; q <= min(issued, stages); ++q) {
+      int s = stage - q;
+      uint32_t ph = phase;
+      if (s < 0) s += stages, ph ^= 1u;
+      volatile int no_abort = 0;
+      wait_bounded(full(s), ph, &no_abort, limit_ns, nullptr, 0);
+    }
+  }
+};
+
+// Sums of two values over the worker threads, in warp order (`red`: used alternately by the caller).
+__device__ __forceinline__ float2 workers_sum2(float a, float b, int workers, float2* red) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+  asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory");
+  a = b = 0.0f;
+  for (int k = 0; k < workers / 32; ++k) a += red[k].x, b += red[k].y;
+  return make_float2(a, b);
+}
+
+// Where column h of the weight lies in shared memory: the first four columns of 32 consecutive packs, then their other
+// four, so that a warp reads 512 consecutive bytes at a time.
+template <int VEC>
+__device__ __forceinline__ int weight_at(int h) {
+  if constexpr (VEC == 4) return h;
+  const int c = h / VEC, half = (h >> 2) & 1;
+  return ((c >> 5) * 64 + half * 32 + (c & 31)) * 4 + (h & 3);
+}
+__host__ __device__ constexpr int weight_floats(int H) { return (H + 255) / 256 * 256; }
+
+// The weight in fp32 (ones where there is none): the whole block.
+template <int VEC>
+__device__ __forceinline__ void weight_to_smem(float* dst, const void* src, int type, int H) {
+  for (int h = threadIdx.x; h < H; h += blockDim.x) {
+    float v = 1.0f;
+    if (src) {
+      if (type == MOE_TYPE_F32) v = static_cast<const float*>(src)[h];
+      else if (type == MOE_TYPE_BF16) v = to_f32<bf16>(static_cast<const bf16*>(src)[h]);
+      else v = to_f32<f16>(static_cast<const f16*>(src)[h]);
+    }
+    dst[weight_at<VEC>(h)] = v;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_weight(const float* v, int pack, f32x2 (&f)[VEC / 2]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) {
+    const float4 w = *reinterpret_cast<const float4*>(v + weight_at<VEC>(pack * VEC + 4 * i));
+    f[2 * i] = f32x2(w.x, w.y);
+    f[2 * i + 1] = f32x2(w.z, w.w);
+  }
+}
+
+template <class T, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+    norm_bwd_ring_kernel(const T* __restrict__ x, int64_t ldx, const void* __restrict__ weight, int param_type,
+                         const float* __restrict__ mean, const float* __restrict__ rstd, const T* __restrict__ dy,
+                         int64_t lddy, T* __restrict__ dx, float* __restrict__ part, int N, int H, int stages,
+                         int* status, int64_t limit_ns) {
+  constexpr int VEC = 16 / sizeof(T), PER = 4, PAIRS = VEC / 2;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ float2 red[2][16];
+  __shared__ int abort_word;
+  const int row_bytes = H * (int)sizeof(T);
+  float* w_s = reinterpret_cast<float*>(ring_mem);
+  uint8_t* places = reinterpret_cast<uint8_t*>(w_s + weight_floats(H));
+  const Ring ring = {smem_u32(places), smem_u32(places) + stages * 2 * row_bytes, stages, 2 * row_bytes, &abort_word, limit_ns, status};
+  const int workers = blockDim.x - 32, warps = workers >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(ring.full(i), 1);
+      mbar_init(ring.empty(i), warps);
+    }
+    abort_word = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  weight_to_smem<VEC>(w_s, weight, param_type, H);
+  __syncthreads();
+  const int lane = threadIdx.x & 31, t = threadIdx.x;
+  if (t >= workers) {
+    if (lane == 0) ring.stream(x, ldx * (int64_t)sizeof(T), dy, lddy * (int64_t)sizeof(T), row_bytes, N);
+    return;
+  }
+  const int packs = H / VEC;
+  const float inv_h = 1.0f / (float)H;
+  f32x2 gw[PER][PAIRS], gb[PER][PAIRS];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) gw[i][j] = gb[i][j] = f32x2(0.0f);
+  int stage = 0, it = 0;
+  uint32_t phase = 0;
+  float mu = 0.0f, rs = 0.0f;
+  if ((int)blockIdx.x < N) mu = mean[blockIdx.x], rs = rstd[blockIdx.x];
+  for (int64_t row = blockIdx.x; row < N; row += gridDim.x, ++it) {
+    const int64_t next = row + gridDim.x;
+    float mu_next = 0.0f, rs_next = 0.0f;
+    if (next < N) mu_next = mean[next], rs_next = rstd[next];
+    // after a wait that ran out the sums are of no use (the status says so); every warp still meets the others below
+    if (lane == 0) wait_bounded(ring.full(stage), phase, ring.abort_flag, limit_ns, status, 803);
+    __syncwarp();
+    const T* at = reinterpret_cast<const T*>(places + (size_t)stage * 2 * row_bytes);
+    f32x2 s2(0.0f), sx2(0.0f);
+    const f32x2 minus_mu(-mu), rs2(rs);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int c = t + i * workers, k = min(c, packs - 1);
+      Pack<T, VEC> rd = load_pack<T, VEC>(at + H + k * VEC);
+      if (c >= packs) rd = zero_pack<T, VEC>();   // dy = 0 adds nothing
+      f32x2 xh[PAIRS], d[PAIRS], w[PAIRS];
+      unpack2<T, VEC>(load_pack<T, VEC>(at + k * VEC), xh);
+      unpack2<T, VEC>(rd, d);
+      load_weight<VEC>(w_s, k, w);
+#pragma unroll
+      for (int j = 0; j < PAIRS; ++j) {
+        xh[j] = mul2(add2(xh[j], minus_mu), rs2);
+        gw[i][j] = fma2(d[j], xh[j], gw[i][j]);
+        gb[i][j] = add2(gb[i][j], d[j]);
+        const f32x2 tw = mul2(d[j], w[j]);
+        s2 = add2(s2, tw);
+        sx2 = fma2(tw, xh[j], sx2);
+      }
+    }
+    if (dx) {
+      const float2 sums = workers_sum2(s2.sum(), sx2.sum(), workers, red[it & 1]);
+      // dx = rs t - rs a - (x - mu) rs^2 b, with a = s / H and b = sx / H; the packs are read from the ring again (kept
+      // in registers beside the sums they spilled)
+      const f32x2 by_x(-rs * rs * (sums.y * inv_h)), by_1(-rs * (sums.x * inv_h));
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = t + i * workers, k = min(c, packs - 1);
+        f32x2 xv[PAIRS], d[PAIRS], w[PAIRS];
+        unpack2<T, VEC>(load_pack<T, VEC>(at + k * VEC), xv);
+        unpack2<T, VEC>(load_pack<T, VEC>(at + H + k * VEC), d);
+        load_weight<VEC>(w_s, k, w);
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j)
+          xv[j] = fma2(mul2(d[j], w[j]), rs2, fma2(add2(xv[j], minus_mu), by_x, by_1));
+        if (c < packs) store_pack<T, VEC>(dx + row * H + (int64_t)c * VEC, pack2<T, VEC>(xv));
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ring.empty(stage));
+    if (++stage == stages) stage = 0, phase ^= 1u;
+    mu = mu_next;
+    rs = rs_next;
+  }
+  if (!part) return;
+  float* out = part + (int64_t)blockIdx.x * 2 * H;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = t + i * workers;
+    if (c < packs) {
+      store_pack<float, VEC>(out + c * VEC, pack2<float, VEC>(gw[i]));
+      store_pack<float, VEC>(out + H + c * VEC, pack2<float, VEC>(gb[i]));
+    }
   }
 }
 
@@ -247,26 +457,42 @@ int norm_validate(const moe_layernorm_config* c) {
 
 constexpr int kMaxBwdBlocks = 152 * 4;
 
-// Threads for `packs` packs a row, at most `per` packs a thread.
+// Threads for `packs` packs a row, at most `per` packs a thread: a warp (four rows a block of 128 threads), else a
+// block of as many warps as it takes for one row.
 RowShape row_shape(int packs, int per) {
   RowShape s;
-  s.tpr = packs <= 32 * per ? 32 : (packs + per - 1) / per;
-  if (s.tpr > 32) s.tpr = s.tpr <= 128 ? 128 : (s.tpr + 127) / 128 * 128;
-  s.block = std::max(s.tpr, 128);
+  s.tpr = packs <= 32 * per ? 32 : ((packs + per - 1) / per + 31) / 32 * 32;
+  s.block = s.tpr == 32 ? 128 : s.tpr;
   s.rows = s.block / s.tpr;
   return s;
 }
 
 int bwd_blocks(int N) { return std::min(N, kMaxBwdBlocks); }
 
-template <class T, class P, int VEC, int PER, int THREADS>
+template <class T, class P, int VEC, int PER, int TPR, int BLOCKS>
 cudaError_t fwd_launch(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight,
                        const void* bias, void* y, float* mean, float* rstd, cudaStream_t s) {
-  const RowShape r = row_shape(c.H / VEC, PER);
-  return launch_pdl(norm_fwd_kernel<T, P, VEC, PER, THREADS>,
-                    dim3((unsigned)((c.N + (int64_t)r.rows - 1) / r.rows)), dim3(r.block), 0, s,
-                    static_cast<const T*>(x), ldx, static_cast<const P*>(weight), static_cast<const P*>(bias),
-                    static_cast<T*>(y), mean, rstd, c.N, c.H, c.eps, r.tpr);
+  constexpr int THREADS = TPR == 32 ? 128 : TPR, ROWS = THREADS / TPR;
+  return launch_pdl(norm_fwd_kernel<T, P, VEC, PER, TPR, THREADS, BLOCKS>,
+                    dim3((unsigned)((c.N + (int64_t)ROWS - 1) / ROWS)), dim3(THREADS), 0, s, static_cast<const T*>(x),
+                    ldx, static_cast<const P*>(weight), static_cast<const P*>(bias), static_cast<T*>(y), mean, rstd, c.N,
+                    c.H, c.eps);
+}
+
+// Up to 256 packs a row stays in one warp, so that no warps have to meet; then in 128, 256 or 1024 threads of up to
+// 16 packs each.
+template <class T, class P, int VEC>
+cudaError_t fwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight, const void* bias,
+                      void* y, float* mean, float* rstd, cudaStream_t s) {
+  const int packs = c.H / VEC;
+  if (packs <= 64) return fwd_launch<T, P, VEC, 2, 32, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 128) return fwd_launch<T, P, VEC, 4, 32, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 256) return fwd_launch<T, P, VEC, 8, 32, 6>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 512) return fwd_launch<T, P, VEC, 4, 128, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 1024) return fwd_launch<T, P, VEC, 8, 128, 6>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 2048) return fwd_launch<T, P, VEC, 8, 256, 3>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 4096) return fwd_launch<T, P, VEC, 16, 256, 2>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  return fwd_launch<T, P, VEC, 16, 1024, 1>(c, x, ldx, weight, bias, y, mean, rstd, s);
 }
 
 template <class T, class P, int VEC, int PER, int THREADS>
@@ -275,7 +501,7 @@ cudaError_t bwd_launch(const moe_layernorm_config& c, const void* x, int64_t ldx
                        int* blocks, cudaStream_t s) {
   const RowShape r = row_shape(c.H / VEC, PER);
   auto kern = norm_bwd_kernel<T, P, VEC, PER, THREADS>;
-  const size_t smem = r.rows > 1 ? 32 * PER * VEC * 8 : 0;   // [2][H], H <= 32 PER VEC; at most 16 KB
+  const size_t smem = r.rows > 1 ? 32 * PER * VEC * 8 : 0;   // [2][H], H <= 32 PER VEC; at most 8 KB
   static std::atomic<int> cached[33];                        // resident blocks an SM by block size
   int per_sm = cached[r.block / 32].load(std::memory_order_relaxed);
   if (per_sm == 0) {
@@ -290,29 +516,72 @@ cudaError_t bwd_launch(const moe_layernorm_config& c, const void* x, int64_t ldx
                     part, c.N, c.H, r.tpr);
 }
 
-// Calls f(T, P, VEC, PER, THREADS) with compile-time values.  vec: rows and parameters take 16-byte packs.
-// Up to 128 packs a row a warp holds it; above, a block with two packs a thread (four where that would
-// pass 1024 threads).
-template <class F>
-cudaError_t with_shape(int type, int param_type, bool vec, int H, F&& f) {
+struct RingShape {
+  int threads, per_sm, stages;
+  size_t smem;
+};
+// Blocks an SM: as many as its registers (128 a thread) and its shared memory hold with three rows in each ring, up to
+// 4.  fixed: bytes beside the ring; row: bytes of a place.
+RingShape ring_shape(int packs, size_t fixed, size_t row) {
+  RingShape r;
+  r.threads = ((packs + 3) / 4 + 31) / 32 * 32 + 32;
+  r.per_sm = std::max(1, std::min(4, 512 / r.threads));
+  auto fits = [&](int per_sm) { return (int)((kRingSm / per_sm - 1024 - 512 - (int)fixed - kRingFixed) / (int64_t)row); };
+  while (r.per_sm > 1 && fits(r.per_sm) < 3) --r.per_sm;
+  r.stages = std::min(kRingMost, fits(r.per_sm));
+  r.smem = fixed + r.stages * row + kRingFixed;
+  return r;
+}
+
+template <class T, int THREADS, int BLOCKS>
+cudaError_t bwd_ring_launch(const moe_layernorm_config& c, const RingShape& r, const void* x, int64_t ldx,
+                            const void* weight, int param_type, const float* mean, const float* rstd, const void* dy,
+                            int64_t lddy, void* dx, float* part, int* blocks, int* status, cudaStream_t s) {
+  auto kern = norm_bwd_ring_kernel<T, THREADS, BLOCKS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)r.smem);
+  if (e != cudaSuccess) return e;
+  *blocks = std::min(bwd_blocks(c.N), r.per_sm * device_sm_count());
+  return launch_pdl(kern, dim3(*blocks), dim3(r.threads), r.smem, s, static_cast<const T*>(x), ldx, weight, param_type,
+                    mean, rstd, static_cast<const T*>(dy), lddy, static_cast<T*>(dx), part, c.N, c.H, r.stages, status,
+                    wait_limit_ns());
+}
+
+// A warp holds rows of up to 128 packs.  Wider rows of 16-byte packs go through the ring of shared memory where a block
+// has threads for them and three places (H up to 13312 in 16 bits, 7680 in fp32); the others stay in a block's
+// registers.
+template <class T, class P, int VEC>
+cudaError_t bwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight, const float* mean,
+                      const float* rstd, const void* dy, int64_t lddy, void* dx, float* part, int* blocks, int* status,
+                      cudaStream_t s) {
+  const int packs = c.H / VEC;
+  if constexpr (VEC > 1) {
+    if (packs <= 32) return bwd_launch<T, P, VEC, 1, 128>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+    if (packs <= 128) return bwd_launch<T, P, VEC, 4, 128>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+    const RingShape r = ring_shape(packs, (size_t)weight_floats(c.H) * 4, 2 * c.H * sizeof(T));
+    const int pt = std::is_same<P, float>::value ? MOE_TYPE_F32 : std::is_same<T, bf16>::value ? MOE_TYPE_BF16 : MOE_TYPE_F16;
+    if (r.threads <= 256 && r.stages >= 3)
+      return bwd_ring_launch<T, 256, 2>(c, r, x, ldx, weight, pt, mean, rstd, dy, lddy, dx, part, blocks, status, s);
+    if (r.threads <= 512 && r.stages >= 3)
+      return bwd_ring_launch<T, 512, 1>(c, r, x, ldx, weight, pt, mean, rstd, dy, lddy, dx, part, blocks, status, s);
+    return bwd_launch<T, P, VEC, 4, 1024>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+  } else {
+    if (packs <= 128) return bwd_launch<T, P, VEC, 4, 128>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+    if (packs <= 4096) return bwd_launch<T, P, VEC, 8, 512>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+    return bwd_launch<T, P, VEC, 16, 1024>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+  }
+}
+
+// Calls f(T, P, VEC) with compile-time values.  vec: rows and parameters take 16-byte packs.  BY_PARAM: a pack is 16
+// bytes of the wider of T and P: fp32 parameters of a 16-bit row are then read 512 consecutive bytes a warp (as packs
+// of eight, two loads with gaps of 16 bytes, they held the forward of 32768 x 7168 at 198 us).
+template <bool BY_PARAM, class F>
+cudaError_t with_pack(int type, int param_type, bool vec, F&& f) {
   return with_type(type, [&](auto tv) {
     using T = decltype(tv);
     auto by_param = [&](auto pv) {
-      constexpr int V = 16 / sizeof(T);
-      auto go = [&](auto v, auto per, auto threads) { return f(tv, pv, v, per, threads); };
-#define MOE_INT(n) std::integral_constant<int, n>{}
-      if (vec) {
-        const int packs = H / V;
-        if (packs <= 32) return go(MOE_INT(V), MOE_INT(1), MOE_INT(128));
-        if (packs <= 64) return go(MOE_INT(V), MOE_INT(2), MOE_INT(128));
-        if (packs <= 128) return go(MOE_INT(V), MOE_INT(4), MOE_INT(128));
-        if (packs <= 1024) return go(MOE_INT(V), MOE_INT(2), MOE_INT(512));
-        return go(MOE_INT(V), MOE_INT(4), MOE_INT(1024));
-      }
-      if (H <= 128) return go(MOE_INT(1), MOE_INT(4), MOE_INT(128));
-      if (H <= 4096) return go(MOE_INT(1), MOE_INT(8), MOE_INT(512));
-      return go(MOE_INT(1), MOE_INT(16), MOE_INT(1024));
-#undef MOE_INT
+      constexpr int wide = BY_PARAM && sizeof(pv) > sizeof(T) ? sizeof(pv) : sizeof(T);
+      if (vec) return f(tv, pv, std::integral_constant<int, 16 / wide>{});
+      return f(tv, pv, std::integral_constant<int, 1>{});
     };
     if (param_type == MOE_TYPE_F32) return by_param(float{});
     return by_param(tv);
@@ -334,7 +603,7 @@ extern "C" {
 int moe_layernorm_workspace_bytes(const moe_layernorm_config* cfg, size_t* bwd_bytes) {
   const int v = norm_validate(cfg);
   if (v != MOE_OK) return v;
-  if (bwd_bytes) *bwd_bytes = align256((size_t)bwd_blocks(cfg->N) * 2 * cfg->H * 4);
+  if (bwd_bytes) *bwd_bytes = sizeof(WsHeader) + align256((size_t)bwd_blocks(cfg->N) * 2 * cfg->H * 4);
   return MOE_OK;
 }
 
@@ -354,9 +623,8 @@ int moe_layernorm_forward(const moe_layernorm_config* cfg, const void* x, int64_
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool vec = vec_rows(x, ldx, c.H, type) && aligned_to(y, 16) && aligned_to(weight, 16) && aligned_to(bias, 16);
   return timed_launch(MOE_K_NORM_FWD, "layer norm", s, [&] {
-    return with_shape(type, param_type, vec, c.H, [&](auto tv, auto pv, auto vv, auto per, auto threads) {
-      return fwd_launch<decltype(tv), decltype(pv), decltype(vv)::value, decltype(per)::value,
-                        decltype(threads)::value>(
+    return with_pack<true>(type, param_type, vec, [&](auto tv, auto pv, auto vv) {
+      return fwd_shape<decltype(tv), decltype(pv), decltype(vv)::value>(
           c, x, ldx, weight, bias, y, mean, rstd, s);
     });
   });
@@ -385,22 +653,20 @@ int moe_layernorm_backward(const moe_layernorm_config* cfg, const void* x, int64
   if (!x || !dy || !mean || !rstd || !aligned_to(x, ts) || !aligned_to(dy, ts) || !aligned_to(dx, ts) ||
       !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return MOE_ERR_INVALID_ARG;
-  if (params) {
-    if (!ws || !aligned_to(ws, 16)) return MOE_ERR_INVALID_ARG;
-    size_t need = 0;
-    moe_layernorm_workspace_bytes(cfg, &need);
-    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  }
+  if (!ws || !aligned_to(ws, 16)) return MOE_ERR_INVALID_ARG;
+  size_t need = 0;
+  moe_layernorm_workspace_bytes(cfg, &need);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!dx && !params) return MOE_OK;
   const bool vec = vec_rows(x, ldx, c.H, type) && vec_rows(dy, lddy, c.H, type) && aligned_to(dx, 16) &&
                    aligned_to(weight, 16);
-  float* part = params ? static_cast<float*>(ws) : nullptr;
+  int* status = static_cast<int*>(ws);
+  float* part = params ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader)) : nullptr;
   int blocks = 0;
   v = timed_launch(MOE_K_NORM_BWD, "layer norm backward", s, [&] {
-    return with_shape(type, param_type, vec, c.H, [&](auto tv, auto pv, auto vv, auto per, auto threads) {
-      return bwd_launch<decltype(tv), decltype(pv), decltype(vv)::value, decltype(per)::value,
-                        decltype(threads)::value>(
-          c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, &blocks, s);
+    return with_pack<false>(type, param_type, vec, [&](auto tv, auto pv, auto vv) {
+      return bwd_shape<decltype(tv), decltype(pv), decltype(vv)::value>(
+          c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, &blocks, status, s);
     });
   });
   if (v != MOE_OK || !params) return v;

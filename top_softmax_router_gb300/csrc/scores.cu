@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(32 * kWarps) scores_bwd_kernel(const T* __rest
       float f[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) f[j] = out[i + j];
-      *reinterpret_cast<Pack<T, VEC>*>(dst + i) = pack<T, VEC>(f);
+      store_pack<T, VEC>(dst + i, pack<T, VEC>(f));
     }
     __syncwarp();
   }

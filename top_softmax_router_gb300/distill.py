@@ -41,6 +41,7 @@ class VocabDistill:
 
     def __init__(self, cfg: DistillConfig, device="cuda"):
         self.cfg = cfg
+        self._c = _args.Structs(cfg)
         self.ws = _args.workspace(max(distill_workspace_bytes(cfg)), device)
 
     def _inputs(self, X, W, ids, teacher):
@@ -58,7 +59,7 @@ class VocabDistill:
         loss = on.empty((n,), torch.float32, X.device)
         lse = on.empty((n,), torch.float32, X.device)
         mean = on.empty((1,), torch.float32, X.device)
-        check(_lib.load().moe_distill_forward(ctypes.byref(c.c_struct(n)), xp, wp, ip, tp, loss.data_ptr(),
+        check(_lib.load().moe_distill_forward(self._c(n), xp, wp, ip, tp, loss.data_ptr(),
                                               lse.data_ptr(), mean.data_ptr(), self.ws.data_ptr(), self.ws.numel(),
                                               on.handle), "moe_distill_forward")
         on.uses(X, W, ids, teacher, self.ws)
@@ -74,7 +75,7 @@ class VocabDistill:
         on = _args.On(stream, X.device)
         dX = on.empty((n, c.H), torch.bfloat16, X.device)
         dW = on.empty((c.V, c.H), dW_dtype, X.device)
-        check(_lib.load().moe_distill_backward(ctypes.byref(c.c_struct(n)), xp, wp, ip, tp, lp, gp, dX.data_ptr(),
+        check(_lib.load().moe_distill_backward(self._c(n), xp, wp, ip, tp, lp, gp, dX.data_ptr(),
                                                dW.data_ptr(), _args.TYPES[dW_dtype], self.ws.data_ptr(),
                                                self.ws.numel(), on.handle), "moe_distill_backward")
         on.uses(X, W, ids, teacher, lse, dloss, self.ws)

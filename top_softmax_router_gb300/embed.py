@@ -40,6 +40,7 @@ class TokenEmbedding:
 
     def __init__(self, cfg: EmbeddingConfig, device="cuda"):
         self.cfg = cfg
+        self._c = _args.Structs(cfg)
         self.ws = _args.workspace(max(embed_workspace_bytes(cfg)), device)
 
     def forward(self, ids, table, stream=None):
@@ -50,7 +51,7 @@ class TokenEmbedding:
         tp = _args.ptr(table, "table", _args.TYPES, (c.V, c.H))
         on = _args.On(stream, table.device)
         y = on.empty((n, c.H), table.dtype, table.device)
-        check(_lib.load().moe_embed_forward(ctypes.byref(c.c_struct(n)), ip, _args.INDEX_TYPES[ids.dtype], tp,
+        check(_lib.load().moe_embed_forward(self._c(n), ip, _args.INDEX_TYPES[ids.dtype], tp,
                                             y.data_ptr(), _args.TYPES[table.dtype], self.ws.data_ptr(),
                                             self.ws.numel(), on.handle), "moe_embed_forward")
         on.uses(ids, table, self.ws)
@@ -66,7 +67,7 @@ class TokenEmbedding:
         on = _args.On(stream, dy.device)
         dW = on.empty((c.V, c.H), torch.float32, dy.device) if into is None else into
         wp = _args.ptr(dW, "into", torch.float32, (c.V, c.H))
-        check(_lib.load().moe_embed_backward(ctypes.byref(c.c_struct(n)), ip, _args.INDEX_TYPES[ids.dtype], gp, ldg,
+        check(_lib.load().moe_embed_backward(self._c(n), ip, _args.INDEX_TYPES[ids.dtype], gp, ldg,
                                              _args.TYPES[dy.dtype], wp, 0 if into is None else 1, self.ws.data_ptr(),
                                              self.ws.numel(), on.handle), "moe_embed_backward")
         on.uses(ids, dy, into, self.ws)

@@ -38,6 +38,7 @@ class LayerNorm:
 
     def __init__(self, cfg: LayerNormConfig, device="cuda"):
         self.cfg = cfg
+        self._c = _args.Structs(cfg)
         self.ws = _args.workspace(layernorm_workspace_bytes(cfg), device)
 
     def _params(self, x, weight, bias):
@@ -59,9 +60,8 @@ class LayerNorm:
         pt = self._params(x, weight, bias)
         on = _args.On(stream, x.device)
         y = on.empty((n, c.H), x.dtype, x.device)
-        stats = on.empty((2, n), torch.float32, x.device)
-        mean, rstd = stats[0], stats[1]
-        check(_lib.load().moe_layernorm_forward(ctypes.byref(c.c_struct(n)), xp, ldx, wp, bp, y.data_ptr(),
+        mean, rstd = on.empty((n,), torch.float32, x.device), on.empty((n,), torch.float32, x.device)
+        check(_lib.load().moe_layernorm_forward(self._c(n), xp, ldx, wp, bp, y.data_ptr(),
                                                 mean.data_ptr(), rstd.data_ptr(), _args.TYPES[x.dtype], pt,
                                                 on.handle), "moe_layernorm_forward")
         on.uses(x, weight, bias)
@@ -82,7 +82,7 @@ class LayerNorm:
         dw = on.empty((c.H,), torch.float32, x.device) if want_dweight else None
         db = on.empty((c.H,), torch.float32, x.device) if want_dbias else None
         check(_lib.load().moe_layernorm_backward(
-            ctypes.byref(c.c_struct(n)), xp, ldx, wp, mp, rp, gp, ldg, dx.data_ptr() if want_dx else None,
+            self._c(n), xp, ldx, wp, mp, rp, gp, ldg, dx.data_ptr() if want_dx else None,
             dw.data_ptr() if want_dweight else None, db.data_ptr() if want_dbias else None, _args.TYPES[x.dtype], pt,
             self.ws.data_ptr(), self.ws.numel(), on.handle), "moe_layernorm_backward")
         on.uses(x, weight, mean, rstd, dy, self.ws)

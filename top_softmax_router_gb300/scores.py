@@ -42,6 +42,7 @@ class ScoreRouter:
 
     def __init__(self, cfg: ScoreRouterConfig, device="cuda"):
         self.cfg = cfg
+        self._c = _args.Structs(cfg)
         b = ctypes.c_size_t()
         check(_lib.load().moe_scores_workspace_bytes(ctypes.byref(cfg.c_struct()), ctypes.byref(b)),
               "moe_scores_workspace_bytes")
@@ -59,7 +60,7 @@ class ScoreRouter:
         idx = on.empty((n, c.k), torch.int32, dev)
         w = on.empty((n, c.k), torch.float32, dev)
         counts = on.empty((c.E,), torch.int32, dev)
-        check(_lib.load().moe_scores_forward(ctypes.byref(c.c_struct(n)), lp, ld, _args.TYPES[logits.dtype], bp,
+        check(_lib.load().moe_scores_forward(self._c(n), lp, ld, _args.TYPES[logits.dtype], bp,
                                              idx.data_ptr(), w.data_ptr(), counts.data_ptr(), self.ws.data_ptr(),
                                              self.ws.numel(), on.handle), "moe_scores_forward")
         on.uses(logits, bias, self.ws)
@@ -74,7 +75,7 @@ class ScoreRouter:
         gp = _args.ptr(dweights, "dweights", torch.float32, (n, c.k))
         on = _args.On(stream, logits.device)
         d = on.empty((n, c.E), logits.dtype, logits.device)
-        check(_lib.load().moe_scores_backward(ctypes.byref(c.c_struct(n)), lp, ld, _args.TYPES[logits.dtype], ip, gp,
+        check(_lib.load().moe_scores_backward(self._c(n), lp, ld, _args.TYPES[logits.dtype], ip, gp,
                                               d.data_ptr(), self.ws.data_ptr(), self.ws.numel(), on.handle),
               "moe_scores_backward")
         on.uses(logits, idx, dweights, self.ws)
