@@ -14,10 +14,6 @@ namespace {
 
 // A row is held in registers by `tpr` threads (a multiple of 32), PER packs of VEC elements each: pack i of
 // thread t holds columns VEC (t + i tpr) ..  A block holds block / tpr rows at a time.
-struct RowShape {
-  int tpr, block, rows;   // threads per row, threads per block, rows per block
-};
-
 // Sums of two values over the tpr threads of a row: one shuffle tree per warp, then the warps' sums in
 // order.  `red`: 2 x 32 floats of shared memory, used alternately by the caller (`slot`).
 __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* red) {
@@ -105,118 +101,113 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 // Persistent: block b takes row groups b, b + grid, ..  x and dy are read once; dx is written, and each
 // thread keeps the sums of dy xh and dy of its columns in registers over all its rows.  The block's sums
 // go to part[block][2][H]; norm_param_kernel adds the blocks in order, so the result has a fixed order.
-template <class T, class P, int VEC, int PER, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) norm_bwd_kernel(const T* __restrict__ x, int64_t ldx,
-                                                       const P* __restrict__ weight, const float* __restrict__ mean,
-                                                       const float* __restrict__ rstd, const T* __restrict__ dy,
-                                                       int64_t lddy, T* __restrict__ dx, float* __restrict__ part,
-                                                       int N, int H, int tpr) {
+// Places past the row (and rows past the last) hold dy = 0, which adds nothing.
+template <class T, class P, int VEC, int PER, int TPR, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+    norm_bwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__ weight, const float* __restrict__ mean,
+                    const float* __restrict__ rstd, const T* __restrict__ dy, int64_t lddy, T* __restrict__ dx,
+                    float* __restrict__ part, int N, int H) {
   pdl_wait();
   pdl_trigger();
+  constexpr int PAIRS = pairs_of<VEC>, ROWS = THREADS / TPR;
   __shared__ float2 red[2][32];
-  extern __shared__ float cols[];   // [2][H]: sums of the block's rows, when it holds several at a time
-  const int t = threadIdx.x % tpr, rpb = blockDim.x / tpr, sub = threadIdx.x / tpr;
-  const int packs = H / VEC;
+  __shared__ float cols[ROWS > 1 ? 2 * 32 * PER * VEC : 1];   // the block's sums, when it holds several rows at a time
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int left = H / VEC - t;   // pack i of the thread is in the row where i TPR < left
   const float inv_h = 1.0f / (float)H;
-  float gw[PER][VEC], gb[PER][VEC];
+  f32x2 gw[PER][PAIRS], gb[PER][PAIRS];
 #pragma unroll
   for (int i = 0; i < PER; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) gw[i][j] = gb[i][j] = 0.0f;
+    for (int j = 0; j < PAIRS; ++j) gw[i][j] = gb[i][j] = f32x2(0.0f);
   int it = 0;
   Pack<T, VEC> nx[PER], nd[PER];   // the next row, loaded while this one is worked on
   float mu_next = 0.0f, rs_next = 0.0f;
   auto load = [&](int64_t row) {
-    if (row >= N) return;
+    const bool ok = row < N;
+    const T* xr = x + row * ldx + t * VEC;
+    const T* dr = dy + row * lddy + t * VEC;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = t + i * tpr;
-      if (c < packs) {
-        nx[i] = load_pack<T, VEC>(x + row * ldx + (int64_t)c * VEC);
-        nd[i] = load_pack<T, VEC>(dy + row * lddy + (int64_t)c * VEC);
+      nx[i] = nd[i] = zero_pack<T, VEC>();
+      if (ok && i * TPR < left) {
+        nx[i] = load_pack<T, VEC>(xr + i * TPR * VEC);
+        nd[i] = load_pack<T, VEC>(dr + i * TPR * VEC);
       }
     }
-    mu_next = mean[row];
-    rs_next = rstd[row];
+    mu_next = ok ? mean[row] : 0.0f;
+    rs_next = ok ? rstd[row] : 0.0f;
   };
-  load((int64_t)blockIdx.x * rpb + sub);
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < N; base += (int64_t)gridDim.x * rpb, ++it) {
+  const P* wt = weight + t * VEC;
+  const bool has_w = weight != nullptr;
+  load((int64_t)blockIdx.x * ROWS + sub);
+  for (int64_t base = (int64_t)blockIdx.x * ROWS; base < N; base += (int64_t)gridDim.x * ROWS, ++it) {
     const int64_t row = base + sub;
-    const bool row_ok = row < N;
     Pack<T, VEC> rx[PER], rd[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) rx[i] = nx[i], rd[i] = nd[i];
-    const float mu = mu_next, rs = rs_next;
-    load(row + (int64_t)gridDim.x * rpb);
-    float s = 0.0f, sx = 0.0f;
+    const f32x2 minus_mu(-mu_next), rs2(rs_next);
+    const float rs = rs_next;
+    load(row + (int64_t)gridDim.x * ROWS);
+    f32x2 s2(0.0f), sx2(0.0f);
+    auto weight_of = [&](int i, f32x2 (&w)[PAIRS]) {
+      Pack<P, VEC> pw = one_pack<P, VEC>();
+      if (has_w && i * TPR < left) pw = load_pack<P, VEC>(wt + i * TPR * VEC);
+      unpack2<P, VEC>(pw, w);
+    };
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int c = t + i * tpr;
-      if (row_ok && c < packs) {
-        float fx[VEC], fd[VEC], fw[VEC];
-        unpack<T, VEC>(rx[i], fx);
-        unpack<T, VEC>(rd[i], fd);
-        if (weight) {
-          Pack<P, VEC> w = load_pack<P, VEC>(weight + c * VEC);
-          unpack<P, VEC>(w, fw);
-        }
+      f32x2 xh[PAIRS], d[PAIRS], w[PAIRS];
+      unpack2<T, VEC>(rx[i], xh);
+      unpack2<T, VEC>(rd[i], d);
+      weight_of(i, w);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (fx[j] - mu) * rs;
-          gw[i][j] = fmaf(fd[j], xh, gw[i][j]);
-          gb[i][j] += fd[j];
-          const float tj = weight ? fd[j] * fw[j] : fd[j];
-          s += tj;
-          sx = fmaf(tj, xh, sx);
-        }
+      for (int j = 0; j < PAIRS; ++j) {
+        xh[j] = mul2(add2(xh[j], minus_mu), rs2);
+        gw[i][j] = fma2(d[j], xh[j], gw[i][j]);
+        gb[i][j] = add2(gb[i][j], d[j]);
+        const f32x2 tw = mul2(d[j], w[j]);
+        s2 = add2(s2, tw);
+        sx2 = fma2(tw, xh[j], sx2);
       }
     }
     if (dx) {
-      const float2 sums = row_sum2(s, sx, tpr, red[it & 1]);
-      const float a = sums.x * inv_h, b = sums.y * inv_h;
+      const float2 sums = row_sum2(s2.sum(), sx2.sum(), TPR, red[it & 1]);
+      const f32x2 by_x(-rs * rs * (sums.y * inv_h)), by_1(-rs * (sums.x * inv_h));
+      T* out = dx + row * H + t * VEC;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int c = t + i * tpr;
-        if (row_ok && c < packs) {
-          float fx[VEC], fd[VEC], fw[VEC], o[VEC];
-          unpack<T, VEC>(rx[i], fx);
-          unpack<T, VEC>(rd[i], fd);
-          if (weight) {
-            Pack<P, VEC> w = load_pack<P, VEC>(weight + c * VEC);
-            unpack<P, VEC>(w, fw);
-          }
+        f32x2 xv[PAIRS], d[PAIRS], w[PAIRS];
+        unpack2<T, VEC>(rx[i], xv);
+        unpack2<T, VEC>(rd[i], d);
+        weight_of(i, w);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float xh = (fx[j] - mu) * rs;
-            const float tj = weight ? fd[j] * fw[j] : fd[j];
-            o[j] = rs * (tj - a - xh * b);
-          }
-          store_pack<T, VEC>(dx + row * H + (int64_t)c * VEC, pack<T, VEC>(o));
-        }
+        for (int j = 0; j < PAIRS; ++j)
+          xv[j] = fma2(mul2(d[j], w[j]), rs2, fma2(add2(xv[j], minus_mu), by_x, by_1));
+        if (row < N && i * TPR < left) store_pack<T, VEC>(out + i * TPR * VEC, pack2<T, VEC>(xv));
       }
     }
   }
   if (!part) return;
   float* out = part + (int64_t)blockIdx.x * 2 * H;
   // the rows of the block are added in turn: row group 0 first
-  for (int r = 0; r < rpb; ++r) {
+  for (int r = 0; r < ROWS; ++r) {
     if (sub == r) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int c = t + i * tpr;
-        if (c < packs) {
+        if (i * TPR < left) {
+          Pack<float, VEC> a = pack2<float, VEC>(gw[i]), b = pack2<float, VEC>(gb[i]);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int h = c * VEC + j;
-            float a = gw[i][j], b = gb[i][j];
-            if (r > 0) a += cols[h], b += cols[H + h];
-            if (r + 1 < rpb) cols[h] = a, cols[H + h] = b;
-            else out[h] = a, out[H + h] = b;
+            const int h = (t + i * TPR) * VEC + j;
+            if (r > 0) a.v[j] += cols[h], b.v[j] += cols[H + h];
+            if (r + 1 < ROWS) cols[h] = a.v[j], cols[H + h] = b.v[j];
+            else out[h] = a.v[j], out[H + h] = b.v[j];
           }
         }
       }
     }
-    if (r + 1 < rpb) __syncthreads();
+    if (r + 1 < ROWS) __syncthreads();
   }
 }
 
@@ -423,30 +414,30 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   }
 }
 
-// dweight[h], dbias[h]: the blocks' partial sums added in a fixed order.  A block owns 32 columns; its 8
-// warps take the partials round robin and their sums are added in warp order.
-__global__ void __launch_bounds__(256) norm_param_kernel(const float* __restrict__ part, float* __restrict__ dweight,
-                                                        float* __restrict__ dbias, int blocks, int H) {
+// dweight[h], dbias[h]: the blocks' partial sums added in a fixed order.  A block owns 32 columns; its 32
+// warps take the partials round robin, and their sums are added in warp order.
+__global__ void __launch_bounds__(1024) norm_param_kernel(const float* __restrict__ part, float* __restrict__ dweight,
+                                                         float* __restrict__ dbias, int blocks, int H) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s[8][32];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;   // column of the [2 H] row of partials
+  const int c = blockIdx.x * 32 + lane;
   const bool second = blockIdx.y == 1;
   float* out = second ? dbias : dweight;
   if (!out) return;
   float a = 0.0f;
   if (c < H) {
     const float* p = part + (second ? H : 0) + c;
-    for (int b = warp; b < blocks; b += 8) a += p[(int64_t)b * 2 * H];
+#pragma unroll 4
+    for (int b = warp; b < blocks; b += 32) a += p[(int64_t)b * 2 * H];
   }
-  s[warp][lane] = a;
+  s[lane][warp] = a;
   __syncthreads();
-  if (warp == 0 && c < H) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) a += s[w][lane];
-    out[c] = a;
-  }
+  // warp w adds the 32 partial sums of column w in a fixed tree
+  a = warp_sum(s[warp][lane]);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < H) out[col] = a;
 }
 
 int norm_validate(const moe_layernorm_config* c) {
@@ -455,17 +446,7 @@ int norm_validate(const moe_layernorm_config* c) {
   return MOE_OK;
 }
 
-constexpr int kMaxBwdBlocks = 152 * 4;
-
-// Threads for `packs` packs a row, at most `per` packs a thread: a warp (four rows a block of 128 threads), else a
-// block of as many warps as it takes for one row.
-RowShape row_shape(int packs, int per) {
-  RowShape s;
-  s.tpr = packs <= 32 * per ? 32 : ((packs + per - 1) / per + 31) / 32 * 32;
-  s.block = s.tpr == 32 ? 128 : s.tpr;
-  s.rows = s.block / s.tpr;
-  return s;
-}
+constexpr int kMaxBwdBlocks = 152 * 4;   // rows of partial sums in the workspace
 
 int bwd_blocks(int N) { return std::min(N, kMaxBwdBlocks); }
 
@@ -480,40 +461,32 @@ cudaError_t fwd_launch(const moe_layernorm_config& c, const void* x, int64_t ldx
 }
 
 // Up to 256 packs a row stays in one warp, so that no warps have to meet; then in 128, 256 or 1024 threads of up to
-// 16 packs each.
+// 16 packs each.  1024 threads an SM (64 registers each): fewer keep too little memory in flight (32768 x 7168 with
+// 768: 189 us, 1024: 164, 1536: 216 as the packs spill).
 template <class T, class P, int VEC>
 cudaError_t fwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight, const void* bias,
                       void* y, float* mean, float* rstd, cudaStream_t s) {
   const int packs = c.H / VEC;
   if (packs <= 64) return fwd_launch<T, P, VEC, 2, 32, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
   if (packs <= 128) return fwd_launch<T, P, VEC, 4, 32, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
-  if (packs <= 256) return fwd_launch<T, P, VEC, 8, 32, 6>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 256) return fwd_launch<T, P, VEC, 8, 32, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
   if (packs <= 512) return fwd_launch<T, P, VEC, 4, 128, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
-  if (packs <= 1024) return fwd_launch<T, P, VEC, 8, 128, 6>(c, x, ldx, weight, bias, y, mean, rstd, s);
-  if (packs <= 2048) return fwd_launch<T, P, VEC, 8, 256, 3>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 1024) return fwd_launch<T, P, VEC, 8, 128, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if (packs <= 2048) return fwd_launch<T, P, VEC, 8, 256, 4>(c, x, ldx, weight, bias, y, mean, rstd, s);
   if (packs <= 4096) return fwd_launch<T, P, VEC, 16, 256, 2>(c, x, ldx, weight, bias, y, mean, rstd, s);
   return fwd_launch<T, P, VEC, 16, 1024, 1>(c, x, ldx, weight, bias, y, mean, rstd, s);
 }
 
-template <class T, class P, int VEC, int PER, int THREADS>
+template <class T, class P, int VEC, int PER, int TPR, int BLOCKS>
 cudaError_t bwd_launch(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight,
                        const float* mean, const float* rstd, const void* dy, int64_t lddy, void* dx, float* part,
                        int* blocks, cudaStream_t s) {
-  const RowShape r = row_shape(c.H / VEC, PER);
-  auto kern = norm_bwd_kernel<T, P, VEC, PER, THREADS>;
-  const size_t smem = r.rows > 1 ? 32 * PER * VEC * 8 : 0;   // [2][H], H <= 32 PER VEC; at most 8 KB
-  static std::atomic<int> cached[33];                        // resident blocks an SM by block size
-  int per_sm = cached[r.block / 32].load(std::memory_order_relaxed);
-  if (per_sm == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, r.block, smem);
-    if (e != cudaSuccess) return e;
-    cached[r.block / 32].store(per_sm = std::max(1, per_sm), std::memory_order_relaxed);
-  }
-  const int64_t groups = ((int64_t)c.N + r.rows - 1) / r.rows;
-  *blocks = (int)std::min<int64_t>(groups, std::min(bwd_blocks(c.N), per_sm * device_sm_count()));
-  return launch_pdl(kern, dim3(*blocks), dim3(r.block), smem, s, static_cast<const T*>(x), ldx,
-                    static_cast<const P*>(weight), mean, rstd, static_cast<const T*>(dy), lddy, static_cast<T*>(dx),
-                    part, c.N, c.H, r.tpr);
+  constexpr int THREADS = TPR == 32 ? 128 : TPR, ROWS = THREADS / TPR;
+  const int64_t groups = ((int64_t)c.N + ROWS - 1) / ROWS;
+  *blocks = (int)std::min<int64_t>(groups, std::min(bwd_blocks(c.N), BLOCKS * device_sm_count()));
+  return launch_pdl(norm_bwd_kernel<T, P, VEC, PER, TPR, THREADS, BLOCKS>, dim3(*blocks), dim3(THREADS), 0, s,
+                    static_cast<const T*>(x), ldx, static_cast<const P*>(weight), mean, rstd,
+                    static_cast<const T*>(dy), lddy, static_cast<T*>(dx), part, c.N, c.H);
 }
 
 struct RingShape {
@@ -555,20 +528,24 @@ cudaError_t bwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx,
                       cudaStream_t s) {
   const int packs = c.H / VEC;
   if constexpr (VEC > 1) {
-    if (packs <= 32) return bwd_launch<T, P, VEC, 1, 128>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
-    if (packs <= 128) return bwd_launch<T, P, VEC, 4, 128>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+#define MOE_BWD(PER, TPR, BLOCKS) \
+  return bwd_launch<T, P, VEC, PER, TPR, BLOCKS>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s)
+    if (packs <= 32) MOE_BWD(1, 32, 4);
+    if (packs <= 128) MOE_BWD(4, 32, 2);
     const RingShape r = ring_shape(packs, (size_t)weight_floats(c.H) * 4, 2 * c.H * sizeof(T));
     const int pt = std::is_same<P, float>::value ? MOE_TYPE_F32 : std::is_same<T, bf16>::value ? MOE_TYPE_BF16 : MOE_TYPE_F16;
     if (r.threads <= 256 && r.stages >= 3)
       return bwd_ring_launch<T, 256, 2>(c, r, x, ldx, weight, pt, mean, rstd, dy, lddy, dx, part, blocks, status, s);
     if (r.threads <= 512 && r.stages >= 3)
       return bwd_ring_launch<T, 512, 1>(c, r, x, ldx, weight, pt, mean, rstd, dy, lddy, dx, part, blocks, status, s);
-    return bwd_launch<T, P, VEC, 4, 1024>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+    MOE_BWD(4, 1024, 1);
   } else {
-    if (packs <= 128) return bwd_launch<T, P, VEC, 4, 128>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
-    if (packs <= 4096) return bwd_launch<T, P, VEC, 8, 512>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
-    return bwd_launch<T, P, VEC, 16, 1024>(c, x, ldx, weight, mean, rstd, dy, lddy, dx, part, blocks, s);
+    if (packs <= 128) MOE_BWD(4, 32, 4);
+    if (packs <= 1024) MOE_BWD(8, 128, 4);
+    if (packs <= 4096) MOE_BWD(8, 512, 1);
+    MOE_BWD(16, 1024, 1);
   }
+#undef MOE_BWD
 }
 
 // Calls f(T, P, VEC) with compile-time values.  vec: rows and parameters take 16-byte packs.  BY_PARAM: a pack is 16
@@ -671,7 +648,7 @@ int moe_layernorm_backward(const moe_layernorm_config* cfg, const void* x, int64
   });
   if (v != MOE_OK || !params) return v;
   return timed_launch(MOE_K_NORM_BWD, "layer norm parameter gradients", s, [&] {
-    return launch_pdl(norm_param_kernel, dim3((c.H + 31) / 32, 2), dim3(256), 0, s, static_cast<const float*>(part),
+    return launch_pdl(norm_param_kernel, dim3((c.H + 31) / 32, 2), dim3(1024), 0, s, static_cast<const float*>(part),
                       dweight, dbias, blocks, c.H);
   });
 }
