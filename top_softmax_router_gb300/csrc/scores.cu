@@ -33,15 +33,38 @@ struct Params {
   float scale;
 };
 
+__device__ __forceinline__ float exp2_approx(float x) {   // PTX ex2.approx: relative error at most 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {    // PTX rcp.approx: relative error at most 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 // What a row's scores are computed from: l -> s.
 struct RowScore {
-  float m, sum;      // softmax: maximum and sum of exp(l - m)
+  float m, sum, inv;   // softmax: maximum, sum of exp(l - m), 1 / sum
   bool sigmoid;
   __device__ __forceinline__ float of(float l) const {
     if (sigmoid) return 1.0f / (1.0f + expf(-l));
     if (m == -INFINITY) return l == l ? 0.0f : l;
     return expf(l - m) / sum;
   }
+  // For the choice: two instructions of the special function unit.  off() bounds how far it is from s.
+  __device__ __forceinline__ float quick(float l) const {
+    if (sigmoid) return rcp_approx(1.0f + exp2_approx(-kLog2e * l));
+    if (m == -INFINITY) return l == l ? 0.0f : l;
+    return exp2_approx((l - m) * kLog2e) * inv;
+  }
+  // sigmoid: the exponent's rounding moves e by 2 x 2^-24 |l| of itself and s by s (1 - s) of that, s (1 - s) |l| <=
+  // 0.23; ex2, the addition and rcp add 2^-22 + 2^-24 + 2^-23 of s: below 2^-21 together.
+  // softmax: the exponent's roundings 3 x 2^-24 x exp(-x) <= 1.2 x 2^-24 of the row's largest score; ex2, the sum of up to
+  // 32 + 5 steps, its reciprocal and the product: 50 x 2^-24 of it: below 2^-18.
+  __device__ __forceinline__ float off() const { return sigmoid ? 0x1p-21f : 0x1p-18f * inv; }
 };
 
 // exp(l - m) of a chosen expert, relative to itself within a few 2^-24 however far l is from m: what the
@@ -103,11 +126,10 @@ __device__ __forceinline__ F group_score(const F* c, int size, int sub, int widt
   return s == s ? s : (F)-INFINITY;
 }
 
-// One warp a row.  Lane t holds experts t, t + 32, ..  The k choices are k rounds of a warp maximum over
-// integer keys (redux), then a warp minimum over the expert ids that have it.  Two fp32 values can be in the
-// wrong order only if they lie within `window` of each other; a round that finds such a candidate beside
-// its choice compares those candidates in fp64 (unless their logit and bias are equal, when the tie rule
-// decides).
+// One warp a row.  Lane t holds experts t, t + 32, .. as integer keys.  The k best are ranked among the few candidates
+// that can be among them (k rounds of a warp maximum over all of them took 148 us for 32768 x 384, k = 8).  Two fp32
+// values can be in the wrong order only if they lie within `window` of each other; where that happens among the
+// candidates they are compared in fp64 (unless their logit and bias are equal, when the tie rule decides).
 template <class T, int PER>
 __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __restrict__ logits, int64_t ld, Params p,
                                                                 int32_t* __restrict__ topk_idx,
@@ -116,6 +138,7 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
   pdl_wait();
   pdl_trigger();
   extern __shared__ double sm[];
+  __shared__ uint2 cands[kWarps][32];   // (key, expert)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
   int* hist = reinterpret_cast<int*>(sm);                                       // [E] choices of this block
   double* vals = sm + (E + 1) / 2 + (int64_t)warp * (p.groups > 1 ? E : 0);      // [E] values of the row's groups
@@ -136,7 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
       l[q] = e < E ? to_f32<T>(lr[e]) : -INFINITY;
       m = fmaxf(m, l[q]);
     }
-    RowScore score = {m, 1.0f, p.sigmoid};
+    RowScore score = {m, 1.0f, 1.0f, p.sigmoid};
     if (!p.sigmoid) {
       m = score.m = key_value(__reduce_max_sync(kFull, order_key(m)));
       float s = 0.0f;
@@ -145,29 +168,27 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
         if (q * 32 + lane < E) s += expf(l[q] - m);
       s = warp_sum(s);
       score.sum = m == -INFINITY ? 1.0f : s;   // every logit masked: all scores are 0
+      score.inv = rcp_approx(score.sum);
     }
-    // Without a bias c grows with l, so the logits themselves order the experts exactly (window 0).
-    // Else |error of c| <= |error of s| + 2^-24 |c|: a sigmoid is at most 2^-22 off (expf 2^-23 relative, an
-    // addition and a division of 2^-24 each; s <= 1), a softmax at most 42 x 2^-24 of the row's largest
-    // score (the exponent's rounding x e^-x <= 0.37, expf, the division and a sum of up to 32 + 5 steps).
-    // Twice that for a pair, and a margin of two.
-    const float window0 = p.bias ? (p.sigmoid ? 0x1p-20f : 0x1p-17f / score.sum) : 0.0f;
+    // Without a bias c grows with l, so the logits themselves order the experts exactly.  Else two values whose fp32
+    // forms are further apart than 2 (off + 2^-24 |c|) are in the right order; the windows below are twice that.
+    const float window0 = p.bias ? 4.0f * score.off() : 0.0f;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int e = q * 32 + lane;
-      key[q] = e < E ? order_key(p.bias ? score.of(l[q]) + __ldg(p.bias + e) : l[q]) : 0u;
+      key[q] = e < E ? order_key(p.bias ? score.quick(l[q]) + __ldg(p.bias + e) : l[q]) : 0u;
     }
     if (p.groups > 1) {
       // values the groups are scored by: c, or s where there is no bias (the logit itself when only the
       // largest counts)
       const bool by_logit = !p.bias && p.group_top == 1;
-      const float wide = by_logit ? 0.0f : 2.0f * (p.sigmoid ? 0x1p-20f : 0x1p-17f / score.sum);
+      const float wide = by_logit ? 0.0f : 8.0f * score.off();
       float* v32 = reinterpret_cast<float*>(vals);
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         const int e = q * 32 + lane;
-        if (e < E) v32[e] = by_logit ? l[q] : p.bias ? (key[q] > 1u ? key_value(key[q]) : NAN) : score.of(l[q]);
+        if (e < E) v32[e] = by_logit ? l[q] : p.bias ? (key[q] > 1u ? key_value(key[q]) : NAN) : score.quick(l[q]);
       }
       __syncwarp();
       const int g = lane / width, sub = lane % width;
@@ -205,60 +226,139 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
         if (!((open_lanes >> (eg * width & 31)) & 1u)) key[q] = 0u;
       }
     }
-    // k rounds
+    // The choice.  Every one of the k best is at least the k-th largest of the lanes' largest keys; what lies that high
+    // (window included), usually little more than k, is gathered, one candidate a lane, and ranked.
     int my_e = 0;
     uint32_t best = 0u;
 #pragma unroll
     for (int q = 0; q < PER; ++q) best = max(best, key[q]);
-    for (int j = 0; j < p.k; ++j) {
-      const uint32_t top = __reduce_max_sync(kFull, best);
-      int q_first = 0;
+    uint32_t floor_key = 1u;
+    {
+      uint32_t left = best;
+      for (int j = 0; j < p.k; ++j) {
+        floor_key = __reduce_max_sync(kFull, left);
+        if (left == floor_key) left = 0u;
+      }
+    }
+    if (p.bias && floor_key > 1u) {
+      const float v = key_value(floor_key);
+      floor_key = order_key(v - (window0 + fabsf(v) * 0x1p-22f));
+    }
+    floor_key = max(floor_key, 1u);
+    uint32_t mine = 0;
 #pragma unroll
-      for (int q = PER - 1; q >= 0; --q)
-        if (key[q] == top) q_first = q;
-      int e = __reduce_min_sync(kFull, best == top ? q_first * 32 + lane : 0x7fffffff);
-      if (p.bias && top > 1u) {
-        const float tv = key_value(top);
-        const uint32_t near_key = order_key(tv - (window0 + fabsf(tv) * 0x1p-22f));
+    for (int q = 0; q < PER; ++q) mine |= (key[q] >= floor_key ? 1u : 0u) << q;
+    int at = __popc(mine), many = at;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kFull, at, off);
+      if (lane >= off) at += v;
+    }
+    const int cand = __shfl_sync(kFull, at, 31);
+    at -= many;
+    if (cand <= 32) {
+      uint2* list = cands[warp];
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if ((mine >> q) & 1u) list[at++] = make_uint2(key[q], (uint32_t)(q * 32 + lane));
+      __syncwarp();
+      const bool is = lane < cand;
+      const uint2 own = is ? list[lane] : make_uint2(0u, 0u);
+      const int own_e = (int)own.y;
+      int rank = 0;
+      for (int j = 0; j < cand; ++j) {
+        const uint2 o = list[j];
+        rank += o.x > own.x || (o.x == own.x && o.y < own.y);
+      }
+      if (p.bias) {
+        // a candidate that another one is too near to be told from in fp32
+        const float v = key_value(own.x);
+        const uint32_t low = own.x > 1u ? order_key(v - (window0 + fabsf(v) * 0x1p-22f)) : 1u;
         bool near = false;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) near |= key[q] >= near_key && q * 32 + lane != e;
+        for (int j = 0; j < cand; ++j) {
+          const uint2 o = list[j];
+          near |= is && own.x > 1u && o.x <= own.x && o.x >= low && (int)o.y != own_e;
+        }
         if (__any_sync(kFull, near)) {
-          const float le = to_f32<T>(lr[e]), be = p.bias[e];
+          // equal logits and biases are no question: the tie rule has decided
+          const float lo = is ? to_f32<T>(lr[own_e]) : 0.0f, bo = is ? p.bias[own_e] : 0.0f;
           bool other = false;
-#pragma unroll
-          for (int q = 0; q < PER; ++q)
-            if (key[q] >= near_key) other |= l[q] != le || p.bias[q * 32 + lane] != be;
+          for (int j = 0; j < cand; ++j) {
+            const uint2 o = list[j];
+            const float lj = __shfl_sync(kFull, lo, j), bj = __shfl_sync(kFull, bo, j);
+            other |= near && o.x <= own.x && o.x >= low && (lj != lo || bj != bo);
+          }
           if (__any_sync(kFull, other)) {
             const ExactScore exact = exact_score<T>(lr, m, p.sigmoid, E);
-            uint32_t mine = 0;
-#pragma unroll
-            for (int q = 0; q < PER; ++q) mine |= (key[q] >= near_key ? 1u : 0u) << q;
-            double bv = -INFINITY;
-            int bq = 0x7fffffff;
-            for (; mine; mine &= mine - 1) {
-              const int i = (__ffs(mine) - 1) * 32 + lane;
-              const double v = exact_value<T>(exact, lr, p.bias, i);
-              if (bq == 0x7fffffff || v > bv) bv = v, bq = i;
+            const double c = is ? exact_value<T>(exact, lr, p.bias, own_e) : 0.0;
+            const bool number = own.x > 1u;
+            rank = 0;
+            for (int j = 0; j < cand; ++j) {
+              const double cj = __shfl_sync(kFull, c, j);
+              const uint2 o = list[j];
+              const bool nj = o.x > 1u;
+              rank += nj != number ? nj : number && cj != c ? cj > c : o.y < own.y;
             }
-            __syncwarp();
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-              const double ov = __shfl_xor_sync(kFull, bv, off);
-              const int oq = __shfl_xor_sync(kFull, bq, off);
-              if (oq != 0x7fffffff && (bq == 0x7fffffff || ov > bv || (ov == bv && oq < bq))) bv = ov, bq = oq;
-            }
-            e = bq;
           }
         }
       }
-      if (lane == j) my_e = e;
-      if ((e & 31) == lane) {
-        best = 0u;
+      __syncwarp();
+      if (is && rank < p.k) list[rank].y = (uint32_t)own_e;   // every lane has its own candidate in registers
+      __syncwarp();
+      if (lane < p.k) my_e = (int)list[lane].y;
+    } else {
+      // many equal values, or k far above the usual: k rounds of a warp maximum
+      for (int j = 0; j < p.k; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        int q_first = 0;
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          if (q == (e >> 5)) key[q] = 0u;
-          best = max(best, key[q]);
+        for (int q = PER - 1; q >= 0; --q)
+          if (key[q] == top) q_first = q;
+        int e = __reduce_min_sync(kFull, best == top ? q_first * 32 + lane : 0x7fffffff);
+        if (p.bias && top > 1u) {
+          const float tv = key_value(top);
+          const uint32_t near_key = order_key(tv - (window0 + fabsf(tv) * 0x1p-22f));
+          bool near = false;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) near |= key[q] >= near_key && q * 32 + lane != e;
+          if (__any_sync(kFull, near)) {
+            const float le = to_f32<T>(lr[e]), be = p.bias[e];
+            bool other = false;
+#pragma unroll
+            for (int q = 0; q < PER; ++q)
+              if (key[q] >= near_key) other |= l[q] != le || p.bias[q * 32 + lane] != be;
+            if (__any_sync(kFull, other)) {
+              const ExactScore exact = exact_score<T>(lr, m, p.sigmoid, E);
+              uint32_t mine = 0;
+#pragma unroll
+              for (int q = 0; q < PER; ++q) mine |= (key[q] >= near_key ? 1u : 0u) << q;
+              double bv = -INFINITY;
+              int bq = 0x7fffffff;
+              for (; mine; mine &= mine - 1) {
+                const int i = (__ffs(mine) - 1) * 32 + lane;
+                const double v = exact_value<T>(exact, lr, p.bias, i);
+                if (bq == 0x7fffffff || v > bv) bv = v, bq = i;
+              }
+              __syncwarp();
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) {
+                const double ov = __shfl_xor_sync(kFull, bv, off);
+                const int oq = __shfl_xor_sync(kFull, bq, off);
+                if (oq != 0x7fffffff && (bq == 0x7fffffff || ov > bv || (ov == bv && oq < bq))) bv = ov, bq = oq;
+              }
+              e = bq;
+            }
+          }
+        }
+        if (lane == j) my_e = e;
+        if ((e & 31) == lane) {
+          best = 0u;
+#pragma unroll
+          for (int q = 0; q < PER; ++q) {
+            if (q == (e >> 5)) key[q] = 0u;
+            best = max(best, key[q]);
+          }
         }
       }
     }
