@@ -86,6 +86,15 @@ def test_against_the_oracle(M, N, H, V, K, P, T):
     compare(run(M, *a, P=P, T=T), *a, T)
 
 
+@pytest.mark.parametrize("N,H,V,P", [(40, 64, 6000, 1), (300, 128, 9000, 2), (256, 320, 5121, 1), (1, 64, 20000, 3)])
+def test_shares_of_a_long_strip(M, N, H, V, P):
+    """Few tiles of dX and many classes: K is split, the last share and strip are short or empty."""
+    a = make(N, H, V, 5, seed=V)
+    out = run(M, *a, P=P)
+    compare(out, *a, 1.0)
+    assert all(torch.equal(p, q) for p, q in zip(out, run(M, *a, P=P)))
+
+
 def test_fp32_weight_gradient(M):
     a = make(200, 128, 600, 8)
     out = run(M, *a, P=2, dt=torch.float32)

@@ -112,6 +112,15 @@ def test_distill_shapes(lib, cfg, code):
     assert lib.load().moe_distill_workspace_bytes(ref(lib.DistillConfig(*cfg)), None, None) == code
 
 
+@pytest.mark.parametrize("H,V,P", [(64, 70000, 1), (1024, 32000, 4), (4096, 65536, 4), (320, 5000, 2), (64, 100, 3)])
+def test_a_distill_workspace_serves_fewer_tokens(lib, H, V, P):
+    f, b, last = ctypes.c_size_t(), ctypes.c_size_t(), (0, 0)
+    for n in list(range(0, 600, 7)) + [1023, 1024, 1025, 2048, 5000, 8192, 30000]:
+        assert lib.load().moe_distill_workspace_bytes(ref(lib.DistillConfig(n, H, V, 8, P, 1.0)), ref(f), ref(b)) == 0
+        assert f.value >= last[0] and b.value >= last[1]
+        last = f.value, b.value
+
+
 def test_distill_arguments(lib):
     L, c = lib.load(), lib.DistillConfig(4, 64, 10, 2, 1, 1.0)
 

@@ -20,6 +20,7 @@ constexpr int kMaxK = 256;
 constexpr int kGroup = 32;        // rows of a bucket
 // Row tiles of a band: the ~76 clusters at work then hold 8 x ~10 tiles, 36 MB of operands at H = 4096.
 constexpr int kHeadBand = 8;
+constexpr int kClusters = 76;     // CTA pairs of the GPU
 
 // One block a group of 32 rows, four rows a warp: q of each entry, equal classes of a row joined at the first of
 // them (class[j] = -1 for every other), the row's sum of q log q, and the group's entries by class tile.
@@ -195,9 +196,28 @@ __global__ void __launch_bounds__(1024) distill_mean_kernel(const float* __restr
   }
 }
 
+// dX = the sum of its shares, in order.
+__global__ void __launch_bounds__(256) distill_join_kernel(const float* __restrict__ acc, uint16_t* __restrict__ dX,
+                                                          int64_t n, int shares) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 256 * 8) {
+    float a[8];
+    unpack<float, 8>(load_pack<float, 8>(acc + i), a);
+    for (int s = 1; s < shares; ++s) {
+      float b[8];
+      unpack<float, 8>(load_pack<float, 8>(acc + (int64_t)s * n + i), b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] += b[j];
+    }
+    store_pack<bf16, 8>(reinterpret_cast<bf16*>(dX) + i, pack<bf16, 8>(a));
+  }
+}
+
 struct DistillLayout {
   int groups, tiles;     // groups of 32 rows; class tiles of 256
   int Vs, S;             // classes a strip (a multiple of 256), strips
+  int splits;            // shares of a strip's classes in the dX GEMM
   size_t q, cls, qlogq, coef, bucket, entry;
   size_t part_m, part_z, entry_logit, fwd_total;
   size_t d, acc, bwd_total;
@@ -210,6 +230,11 @@ DistillLayout distill_layout(const moe_distill_config& c) {
   L.tiles = (int)((V + 255) / 256);
   L.Vs = (int)(((V + c.P - 1) / c.P + 255) / 256 * 256);
   L.S = (int)((V + L.Vs - 1) / L.Vs);
+  // dX has N x H tiles of 256 x 256 and a long K: where its tiles fill less than half of the 76 clusters, each strip's
+  // K is split among them, at least 8 blocks of 64 classes to a share.  (2048 x 1024 from 8192 classes a strip, 32
+  // tiles: 58 us a strip unsplit.)
+  const int64_t tiles_n = (c.H + 255) / 256, dx_tiles = ((N + 255) / 256) * tiles_n;
+  L.splits = (int)std::max<int64_t>(1, std::min<int64_t>(L.Vs / 512, dx_tiles > 0 ? kClusters / dx_tiles : 1));
   size_t o = align256(sizeof(WsHeader));
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -229,7 +254,10 @@ DistillLayout distill_layout(const moe_distill_config& c) {
   L.fwd_total = o;
   o = common;
   L.d = take((size_t)N * L.Vs * 2);
-  L.acc = take(L.S > 1 ? (size_t)N * c.H * 4 : 0);
+  // rows of fp32: N, or shares x N of any smaller N (a workspace serves fewer tokens too)
+  const int64_t most = std::min<int64_t>(L.Vs / 512, kClusters / tiles_n);   // shares of a single row tile
+  const int64_t rows = std::max<int64_t>(L.S > 1 ? N : 0, most > 1 ? std::min<int64_t>(N * most, 256 * kClusters / tiles_n) : 0);
+  L.acc = take((size_t)rows * c.H * 4);
   L.bwd_total = o;
   return L;
 }
@@ -382,8 +410,9 @@ int moe_distill_backward(const moe_distill_config* cfg, const uint16_t* X, const
     x.M = c.N;
     x.N = c.H;
     x.nk = (width + GEMM_BK - 1) / GEMM_BK;
+    x.splits = L.splits;
     x.add = st > 0 ? acc : nullptr;
-    if (st + 1 < L.S) x.out32 = acc;
+    if (st + 1 < L.S || L.splits > 1) x.out32 = acc;
     else x.out16 = dX;
     x.ldo = c.H;
     if ((v = timed_launch(MOE_K_DISTILL_DX, "distill dX", s, [&] {
@@ -402,7 +431,12 @@ int moe_distill_backward(const moe_distill_config* cfg, const uint16_t* X, const
          })) != MOE_OK)
       return v;
   }
-  return MOE_OK;
+  if (L.splits == 1) return MOE_OK;
+  return timed_launch(MOE_K_DISTILL_DX, "distill dX shares", s, [&] {
+    const int64_t n = (int64_t)c.N * c.H;
+    return launch_pdl(distill_join_kernel, dim3((unsigned)std::min<int64_t>((n / 8 + 255) / 256, sms * 8)), dim3(256), 0, s,
+                      static_cast<const float*>(acc), dX, n, L.splits);
+  });
 }
 
 }  // extern "C"

@@ -26,6 +26,7 @@ enum HeadEpi : int {
 struct HeadGemm {
   int M, N, nk;              // rows, columns, K blocks of 64
   int tiles_m, tiles_n, band;
+  int splits;                // HEAD_OUT: shares of K, each with its own output (1: no split)
   int* status;
   int64_t limit_ns;
   // HEAD_LSE, HEAD_D
@@ -43,8 +44,8 @@ struct HeadGemm {
   uint16_t* d;               // [M][ldd]
   int ldd;
   // HEAD_OUT
-  const float* add;          // [M][ldo] or NULL
-  float* out32;              // [M][ldo] or NULL
+  const float* add;          // [splits][M][ldo] or NULL
+  float* out32;              // [splits][M][ldo] or NULL
   uint16_t* out16;           // [M][ldo] or NULL
   int ldo;
 };
@@ -75,9 +76,11 @@ __device__ __forceinline__ float tc_ld1(uint32_t taddr) {
   return __uint_as_float(r);
 }
 
-// The epilogue of one warp: rows row0 + lane (valid below p.M), the columns c0 .. c0 + 127 of column tile nt.
+// The epilogue of one warp: rows row0 + lane (valid below p.M), the columns c0 .. c0 + 127 of column tile nt.  none: the
+// tile's share of K is empty, and its accumulator holds nothing.
 template <int EPI>
-__device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int nt, int half, uint32_t tacc, int lane) {
+__device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int nt, int half, int split, bool none,
+                                              uint32_t tacc, int lane) {
   const int row = row0 + lane;
   const bool ok = row < p.M;
   const int n0 = nt * 256;
@@ -131,11 +134,15 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
       }
     }
   } else {
-    const int64_t at = (int64_t)row * p.ldo + n0;
+    const int64_t at = ((int64_t)split * p.M + row) * p.ldo + n0;
 #pragma unroll 1
     for (int c = c0; c < c1; c += 32) {               // N is a multiple of 32 here
       tc_ld32(tacc + c, v);
       if (!ok) continue;
+      if (none) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+      }
       if (p.add) {
         const float4* a = reinterpret_cast<const float4*>(p.add + at + c);
 #pragma unroll
@@ -168,8 +175,14 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
 }
 
 // Tile w: bands of p.band row tiles; within a band the row tile varies fastest, so that the clusters at work share a
-// few tiles of A and of B, which stay in L2.
-__device__ __forceinline__ void head_tile(const HeadGemm& p, int w, int* mt, int* nt) {
+// few tiles of A and of B, which stay in L2.  K blocks [kb0, kb1); with splits, all tiles of a share come before the
+// next share's.
+__device__ __forceinline__ void head_tile(const HeadGemm& p, int w, int* mt, int* nt, int* kb0, int* kb1, int* split) {
+  const int tiles = p.tiles_m * p.tiles_n, per_split = (p.nk + p.splits - 1) / p.splits;
+  *split = w / tiles;
+  w -= *split * tiles;
+  *kb0 = min(p.nk, *split * per_split);
+  *kb1 = min(p.nk, *kb0 + per_split);
   const int per_band = p.band * p.tiles_n;
   const int b = w / per_band, rem = w - b * per_band;
   const int in_band = min(p.band, p.tiles_m - b * p.band);
@@ -227,7 +240,7 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();                                       // no global memory access before this point
 
-  const int total = p.tiles_m * p.tiles_n;
+  const int total = p.tiles_m * p.tiles_n * p.splits;
   if (warp == 0) {
     // ------------------------------------------------------------ loads (both CTAs)
     if (lane == 0) {
@@ -235,10 +248,10 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int w = cluster; w < total && ok; w += clusters) {
-        int mt, nt;
-        head_tile(p, w, &mt, &nt);
+        int mt, nt, kb0, kb1, split;
+        head_tile(p, w, &mt, &nt, &kb0, &kb1, &split);
         const int row = mt * 256 + 128 * (int)rank, col = nt * 256 + 128 * (int)rank;
-        for (int kb = 0; kb < p.nk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.limit_ns, p.status, 701)) {
             ok = false;
             break;
@@ -286,7 +299,9 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
         if (!__shfl_sync(0xffffffffu, good, 0)) break;
         tc_fence_after();
         const uint32_t tacc = tmem_base + acc * 256;
-        for (int kb = 0; kb < p.nk; ++kb) {
+        int mt, nt, kb0, kb1, split;
+        head_tile(p, w, &mt, &nt, &kb0, &kb1, &split);
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (lane == 0) good = wait_bounded(full_bar(stage), phase, abort_flag, p.limit_ns, p.status, 703);
           if (!__shfl_sync(0xffffffffu, good, 0)) {
             ok = false;
@@ -299,7 +314,7 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
             for (int kk = 0; kk < GEMM_BK / 16; ++kk) {
               const uint64_t ad = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024) : smem_desc_sw128(sa + kk * 32, 0, 1024);
               const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 0, 1024);
-              tc_mma_pair(tacc, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+              tc_mma_pair(tacc, ad, bd, idesc, kb != kb0 || kk != 0 ? 1u : 0u);
             }
             tc_commit_pair(empty_bar(stage), 0x3);
           }
@@ -327,9 +342,9 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
       if (lane == 0) good = wait_bounded(tfull_bar(acc), (it >> 1) & 1, abort_flag, p.limit_ns, p.status, 704);
       if (!__shfl_sync(0xffffffffu, good, 0)) break;
       tc_fence_after();
-      int mt, nt;
-      head_tile(p, w, &mt, &nt);
-      head_epilogue<EPI>(p, mt * 256 + 128 * (int)rank + q * 32, nt, half,
+      int mt, nt, kb0, kb1, split;
+      head_tile(p, w, &mt, &nt, &kb0, &kb1, &split);
+      head_epilogue<EPI>(p, mt * 256 + 128 * (int)rank + q * 32, nt, half, split, kb0 == kb1,
                          tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256, lane);
       tc_fence_before();
       __syncwarp();
@@ -351,7 +366,8 @@ cudaError_t launch_head_gemm(const CUtensorMap& a, const CUtensorMap& b, HeadGem
   auto kern = head_gemm_kernel<EPI, A_MN, B_MN>;
   p.tiles_m = (p.M + 255) / 256;
   p.tiles_n = (p.N + 255) / 256;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  if (p.splits < 1) p.splits = 1;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadSmem::TOTAL);
   if (err != cudaSuccess) return err;

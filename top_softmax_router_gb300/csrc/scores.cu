@@ -21,6 +21,13 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+// The same in three instructions for a value that is not -0; a NaN comes out beyond an infinity, and nan_last() puts it
+// in its place.
+__device__ __forceinline__ uint32_t quick_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint32_t nan_last(uint32_t k) { return k > 0xff800000u || k < 0x007fffffu ? 1u : k; }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
@@ -55,10 +62,10 @@ struct RowScore {
     return expf(l - m) / sum;
   }
   // For the choice: two instructions of the special function unit.  off() bounds how far it is from s.
-  __device__ __forceinline__ float quick(float l) const {
-    if (sigmoid) return rcp_approx(1.0f + exp2_approx(-kLog2e * l));
-    if (m == -INFINITY) return l == l ? 0.0f : l;
-    return exp2_approx((l - m) * kLog2e) * inv;
+  __device__ __forceinline__ float quick_sigmoid(float l) const { return rcp_approx(1.0f + exp2_approx(-kLog2e * l)); }
+  __device__ __forceinline__ float quick_softmax(float l) const {
+    const float s = exp2_approx((l - m) * kLog2e) * inv;
+    return l == -INFINITY ? 0.0f : s;   // also where every logit is
   }
   // sigmoid: the exponent's rounding moves e by 2 x 2^-24 |l| of itself and s by s (1 - s) of that, s (1 - s) |l| <=
   // 0.23; ex2, the addition and rcp add 2^-22 + 2^-24 + 2^-23 of s: below 2^-21 together.
@@ -126,77 +133,172 @@ __device__ __forceinline__ F group_score(const F* c, int size, int sub, int widt
   return s == s ? s : (F)-INFINITY;
 }
 
-// One warp a row.  Lane t holds experts t, t + 32, .. as integer keys.  The k best are ranked among the few candidates
+// The score of the lane's group in fp64, from each lane's `per` experts from `first` on.
+template <class T>
+__device__ __noinline__ double group_score_run(const ExactScore x, const T* lr, const float* bias, int first, int per,
+                                               int width, int top, int size) {
+  double m1 = -INFINITY, m2 = -INFINITY;
+  for (int i = 0; i < per; ++i) {
+    const double v = exact_value<T>(x, lr, bias, first + i);
+    if (v > m1) m2 = m1, m1 = v;
+    else if (v > m2) m2 = v;
+  }
+  for (int off = 1; off < width; off <<= 1) {
+    const double o1 = __shfl_xor_sync(kFull, m1, off), o2 = __shfl_xor_sync(kFull, m2, off);
+    const double lo = m1 > o1 ? o1 : m1, second = m1 > o1 ? m2 : o2;
+    m1 = m1 > o1 ? m1 : o1;
+    m2 = lo > second ? lo : second;
+  }
+  const double s = top == 2 && size > 1 ? m1 + m2 : m1;
+  return s == s ? s : -INFINITY;
+}
+
+// One warp a row, its experts' values as integer keys in the lanes' registers.  The k best are ranked among the few candidates
 // that can be among them (k rounds of a warp maximum over all of them took 148 us for 32768 x 384, k = 8).  Two fp32
 // values can be in the wrong order only if they lie within `window` of each other; where that happens among the
 // candidates they are compared in fp64 (unless their logit and bias are equal, when the tie rule decides).
-template <class T, int PER>
-__global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __restrict__ logits, int64_t ld, Params p,
-                                                                int32_t* __restrict__ topk_idx,
-                                                                float* __restrict__ weights,
-                                                                int32_t* __restrict__ counts) {
+
+// Blocks an SM.
+constexpr int fwd_blocks(int per) { return per <= 4 ? 4 : per <= 12 ? 4 : per <= 16 ? 2 : 1; }
+
+// RUN: lane t holds the PER = E / 32 consecutive experts from t PER on, so that a lane's experts are of one group and the
+// groups are scored in registers.  Else lane t holds experts t, t + 32, .. and the groups are scored from shared memory.
+template <class T, int PER, bool RUN>
+__global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
+    scores_fwd_kernel(const T* __restrict__ logits, int64_t ld, Params p, int32_t* __restrict__ topk_idx,
+                      float* __restrict__ weights, int32_t* __restrict__ counts) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ double sm[];
   __shared__ uint2 cands[kWarps][32];   // (key, expert)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = p.E;
   int* hist = reinterpret_cast<int*>(sm);                                       // [E] choices of this block
-  double* vals = sm + (E + 1) / 2 + (int64_t)warp * (p.groups > 1 ? E : 0);      // [E] values of the row's groups
+  double* vals = sm + (E + 1) / 2 + (int64_t)warp * (!RUN && p.groups > 1 ? E : 0);   // [E] values of the row's groups
+  auto expert = [&](int q) { return RUN ? lane * PER + q : q * 32 + lane; };
+  auto held = [&](int q) { return RUN || q * 32 + lane < E; };
   if (counts) {
     for (int e = threadIdx.x; e < E; e += 32 * kWarps) hist[e] = 0;
     __syncthreads();
   }
+  const bool biased = p.bias != nullptr;
+  constexpr bool KEEP_BIAS = PER <= 16;   // in registers over the warp's rows
+  float bias[KEEP_BIAS ? PER : 1];
+  if constexpr (KEEP_BIAS) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) bias[q] = biased && held(q) ? __ldg(p.bias + expert(q)) : 0.0f;
+  }
   int width = 32;                 // lanes a group: 32 / (groups rounded up to a power of two)
   while (width > 1 && width * p.groups > 32) width >>= 1;
+  // the scores enter the choice, or the weights as they are
+  const bool by_score = !biased && p.groups > 1 && p.group_top == 2;
+  const bool need_scores = biased || by_score || !p.renormalize;
   for (int64_t row = (int64_t)blockIdx.x * kWarps + warp; row < p.N; row += (int64_t)gridDim.x * kWarps) {
     const T* lr = logits + row * ld;
     float l[PER];
     uint32_t key[PER];
-    float m = -INFINITY;
+    if constexpr (RUN) {
+      constexpr int CH = PER % 4 == 0 ? 4 : PER;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int e = q * 32 + lane;
-      l[q] = e < E ? to_f32<T>(lr[e]) : -INFINITY;
-      m = fmaxf(m, l[q]);
+      for (int q = 0; q < PER; q += CH) {
+        float f[CH];
+        unpack<T, CH>(load_pack<T, CH>(lr + lane * PER + q), f);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) l[q + j] = f[j];
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) l[q] = held(q) ? to_f32<T>(lr[expert(q)]) : -INFINITY;
     }
+    float m = -INFINITY;
     RowScore score = {m, 1.0f, 1.0f, p.sigmoid};
-    if (!p.sigmoid) {
+    if (!p.sigmoid && need_scores) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) m = fmaxf(m, l[q]);
       m = score.m = key_value(__reduce_max_sync(kFull, order_key(m)));
       float s = 0.0f;
 #pragma unroll
       for (int q = 0; q < PER; ++q)
-        if (q * 32 + lane < E) s += expf(l[q] - m);
+        if (held(q)) s += expf(l[q] - m);
       s = warp_sum(s);
       score.sum = m == -INFINITY ? 1.0f : s;   // every logit masked: all scores are 0
       score.inv = rcp_approx(score.sum);
     }
     // Without a bias c grows with l, so the logits themselves order the experts exactly.  Else two values whose fp32
     // forms are further apart than 2 (off + 2^-24 |c|) are in the right order; the windows below are twice that.
-    const float window0 = p.bias ? 4.0f * score.off() : 0.0f;
+    const float window0 = biased ? 4.0f * score.off() : 0.0f;
+    // (The uniform cases stand outside the loops: a branch in each step would run the steps one after the other.)
+    float s_q[PER];
+    if (biased || by_score) {
+      if (p.sigmoid) {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int e = q * 32 + lane;
-      key[q] = e < E ? order_key(p.bias ? score.quick(l[q]) + __ldg(p.bias + e) : l[q]) : 0u;
+        for (int q = 0; q < PER; ++q) s_q[q] = score.quick_sigmoid(l[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < PER; ++q) s_q[q] = score.quick_softmax(l[q]);
+      }
+    }
+    bool odd = false;   // a NaN, which the quick keys put at an end
+    auto set_key = [&](int q, float c) {
+      key[q] = held(q) ? quick_key(c) : 0u;
+      odd |= c != c;
+    };
+    if (biased) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        set_key(q, s_q[q] + (KEEP_BIAS ? bias[KEEP_BIAS ? q : 0] : held(q) ? __ldg(p.bias + expert(q)) : 0.0f));
+    } else {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) set_key(q, l[q] + 0.0f);
+    }
+    odd = __any_sync(kFull, odd);
+    if (odd) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) key[q] = held(q) ? nan_last(key[q]) : 0u;
     }
     if (p.groups > 1) {
       // values the groups are scored by: c, or s where there is no bias (the logit itself when only the
       // largest counts)
-      const bool by_logit = !p.bias && p.group_top == 1;
-      const float wide = by_logit ? 0.0f : 8.0f * score.off();
-      float* v32 = reinterpret_cast<float*>(vals);
-      __syncwarp();
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const int e = q * 32 + lane;
-        if (e < E) v32[e] = by_logit ? l[q] : p.bias ? (key[q] > 1u ? key_value(key[q]) : NAN) : score.quick(l[q]);
-      }
-      __syncwarp();
+      const float wide = biased || by_score ? 8.0f * score.off() : 0.0f;
       const int g = lane / width, sub = lane % width;
       const bool mine = g < p.groups;
-      const float gs = group_score<float>(v32 + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+      float gs;
+      if constexpr (RUN) {
+        uint32_t k1 = 1u, k2 = 1u;   // the two largest keys
+        if (by_score) {
+#pragma unroll
+          for (int q = 0; q < PER; ++q) {
+            const uint32_t k = nan_last(quick_key(s_q[q]));
+            k2 = max(k2, min(k1, k));
+            k1 = max(k1, k);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < PER; ++q) {
+            k2 = max(k2, min(k1, key[q]));
+            k1 = max(k1, key[q]);
+          }
+        }
+        for (int off = 1; off < width; off <<= 1) {
+          const uint32_t o1 = __shfl_xor_sync(kFull, k1, off), o2 = __shfl_xor_sync(kFull, k2, off);
+          k2 = max(min(k1, o1), max(k2, o2));
+          k1 = max(k1, o1);
+        }
+        const float v1 = k1 > 1u ? key_value(k1) : -INFINITY, v2 = k2 > 1u ? key_value(k2) : -INFINITY;
+        gs = p.group_top == 2 && p.group_size > 1 ? v1 + v2 : v1;
+        if (gs != gs) gs = -INFINITY;
+      } else {
+        float* v32 = reinterpret_cast<float*>(vals);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+          if (held(q)) v32[expert(q)] = by_score ? s_q[q] : key[q] > 1u ? key_value(key[q]) : NAN;
+        __syncwarp();
+        gs = group_score<float>(v32 + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+      }
       const float w = wide + fabsf(gs) * (wide > 0.0f ? 0x1p-21f : 0.0f);
       // rank of the group: how many are surely before it, and how many may be
       int before = 0, sure = 0, maybe = 0;
+#pragma unroll 4
       for (int h = 0; h < p.groups; ++h) {
         const float o = __shfl_sync(kFull, gs, h * width);
         before += o > gs || (o == gs && h < g);
@@ -207,11 +309,15 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
       const bool unsure = mine && wide > 0.0f && sure < p.topk_groups && maybe >= p.topk_groups;
       if (__any_sync(kFull, unsure)) {
         const ExactScore exact = exact_score<T>(lr, m, p.sigmoid, E);
-        __syncwarp();
-        for (int e = lane; e < E; e += 32) vals[e] = exact_value<T>(exact, lr, p.bias, e);
-        __syncwarp();
-        const double gd =
-            group_score<double>(vals + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+        double gd;
+        if constexpr (RUN) {
+          gd = group_score_run<T>(exact, lr, p.bias, lane * PER, PER, width, p.group_top, p.group_size);
+        } else {
+          __syncwarp();
+          for (int e = lane; e < E; e += 32) vals[e] = exact_value<T>(exact, lr, p.bias, e);
+          __syncwarp();
+          gd = group_score<double>(vals + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+        }
         before = 0;
         for (int h = 0; h < p.groups; ++h) {
           const double o = __shfl_sync(kFull, gd, h * width);
@@ -219,11 +325,16 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
         }
         open = mine && before < p.topk_groups;
       }
-      const uint32_t open_lanes = __ballot_sync(kFull, open);
+      if constexpr (RUN) {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const uint32_t eg = ((uint32_t)(q * 32 + lane) * p.group_inv) >> 20;
-        if (!((open_lanes >> (eg * width & 31)) & 1u)) key[q] = 0u;
+        for (int q = 0; q < PER; ++q) key[q] = open ? key[q] : 0u;
+      } else {
+        const uint32_t open_lanes = __ballot_sync(kFull, open);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          const uint32_t eg = ((uint32_t)(q * 32 + lane) * p.group_inv) >> 20;
+          if (!((open_lanes >> (eg * width & 31)) & 1u)) key[q] = 0u;
+        }
       }
     }
     // The choice.  Every one of the k best is at least the k-th largest of the lanes' largest keys; what lies that high
@@ -240,7 +351,7 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
         if (left == floor_key) left = 0u;
       }
     }
-    if (p.bias && floor_key > 1u) {
+    if (biased && floor_key > 1u) {
       const float v = key_value(floor_key);
       floor_key = order_key(v - (window0 + fabsf(v) * 0x1p-22f));
     }
@@ -261,25 +372,24 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < PER; ++q)
-        if ((mine >> q) & 1u) list[at++] = make_uint2(key[q], (uint32_t)(q * 32 + lane));
+        if ((mine >> q) & 1u) list[at++] = make_uint2(key[q], (uint32_t)expert(q));
       __syncwarp();
       const bool is = lane < cand;
       const uint2 own = is ? list[lane] : make_uint2(0u, 0u);
       const int own_e = (int)own.y;
-      int rank = 0;
+      // rank, and whether another candidate is too near to be told from this one in fp32
+      const float v = key_value(own.x);
+      const uint32_t low = biased && own.x > 1u ? order_key(v - (window0 + fabsf(v) * 0x1p-22f)) : own.x;
+      int rank = 0, close = 0;
+#pragma unroll 4
       for (int j = 0; j < cand; ++j) {
         const uint2 o = list[j];
-        rank += o.x > own.x || (o.x == own.x && o.y < own.y);
+        const bool above = o.x > own.x || (o.x == own.x && o.y < own.y);
+        rank += above;
+        close += !above && o.x >= low;    // itself among them
       }
-      if (p.bias) {
-        // a candidate that another one is too near to be told from in fp32
-        const float v = key_value(own.x);
-        const uint32_t low = own.x > 1u ? order_key(v - (window0 + fabsf(v) * 0x1p-22f)) : 1u;
-        bool near = false;
-        for (int j = 0; j < cand; ++j) {
-          const uint2 o = list[j];
-          near |= is && own.x > 1u && o.x <= own.x && o.x >= low && (int)o.y != own_e;
-        }
+      if (biased) {
+        const bool near = is && own.x > 1u && close > 1;
         if (__any_sync(kFull, near)) {
           // equal logits and biases are no question: the tie rule has decided
           const float lo = is ? to_f32<T>(lr[own_e]) : 0.0f, bo = is ? p.bias[own_e] : 0.0f;
@@ -315,19 +425,19 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
 #pragma unroll
         for (int q = PER - 1; q >= 0; --q)
           if (key[q] == top) q_first = q;
-        int e = __reduce_min_sync(kFull, best == top ? q_first * 32 + lane : 0x7fffffff);
-        if (p.bias && top > 1u) {
+        int e = __reduce_min_sync(kFull, best == top ? expert(q_first) : 0x7fffffff);
+        if (biased && top > 1u) {
           const float tv = key_value(top);
           const uint32_t near_key = order_key(tv - (window0 + fabsf(tv) * 0x1p-22f));
           bool near = false;
 #pragma unroll
-          for (int q = 0; q < PER; ++q) near |= key[q] >= near_key && q * 32 + lane != e;
+          for (int q = 0; q < PER; ++q) near |= key[q] >= near_key && expert(q) != e;
           if (__any_sync(kFull, near)) {
             const float le = to_f32<T>(lr[e]), be = p.bias[e];
             bool other = false;
 #pragma unroll
             for (int q = 0; q < PER; ++q)
-              if (key[q] >= near_key) other |= l[q] != le || p.bias[q * 32 + lane] != be;
+              if (key[q] >= near_key) other |= l[q] != le || p.bias[expert(q)] != be;
             if (__any_sync(kFull, other)) {
               const ExactScore exact = exact_score<T>(lr, m, p.sigmoid, E);
               uint32_t mine = 0;
@@ -336,7 +446,7 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
               double bv = -INFINITY;
               int bq = 0x7fffffff;
               for (; mine; mine &= mine - 1) {
-                const int i = (__ffs(mine) - 1) * 32 + lane;
+                const int i = expert(__ffs(mine) - 1);
                 const double v = exact_value<T>(exact, lr, p.bias, i);
                 if (bq == 0x7fffffff || v > bv) bv = v, bq = i;
               }
@@ -352,17 +462,17 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
           }
         }
         if (lane == j) my_e = e;
-        if ((e & 31) == lane) {
+        if ((RUN ? e / PER : e & 31) == lane) {
           best = 0u;
 #pragma unroll
           for (int q = 0; q < PER; ++q) {
-            if (q == (e >> 5)) key[q] = 0u;
+            if (expert(q) == e) key[q] = 0u;
             best = max(best, key[q]);
           }
         }
       }
     }
-    // weights, the sum in slot order
+    // weights; a lane without a slot adds 0
     const float ls = lane < p.k ? to_f32<T>(lr[my_e]) : -INFINITY;
     float s = 0.0f, total = 1.0f;
     if (p.sigmoid || !p.renormalize) {
@@ -371,8 +481,7 @@ __global__ void __launch_bounds__(32 * kWarps) scores_fwd_kernel(const T* __rest
       s = chosen_exp(ls, key_value(__reduce_max_sync(kFull, order_key(ls))));   // the row's sum cancels
     }
     if (p.renormalize) {
-      total = 0.0f;
-      for (int j = 0; j < p.k; ++j) total += __shfl_sync(kFull, s, j);
+      total = warp_sum(s);
     }
     if (lane < p.k) {
       topk_idx[row * p.k + lane] = my_e;
@@ -492,9 +601,9 @@ Params params(const moe_scores_config& c, const float* bias) {
   return p;
 }
 
-unsigned row_blocks(int N) {
+unsigned row_blocks(int N, int per_sm) {
   const int64_t need = ((int64_t)N + kWarps - 1) / kWarps;
-  return (unsigned)std::min<int64_t>(need, (int64_t)device_sm_count() * 8);
+  return (unsigned)std::min<int64_t>(need, (int64_t)device_sm_count() * per_sm);
 }
 
 template <class F>
@@ -546,15 +655,21 @@ int moe_scores_forward(const moe_scores_config* cfg, const void* logits, int64_t
     return with_type(type, [&](auto tv) {
       using T = decltype(tv);
       return with_per(c.E, [&](auto per) {
-        auto kern = scores_fwd_kernel<T, decltype(per)::value>;
-        // [E] counters, then [E] values a warp where there are groups: at most 4 KB + 64 KB
-        const size_t smem = ((size_t)(c.E + 1) / 2 + (p.groups > 1 ? (size_t)kWarps * c.E : 0)) * 8;
-        if (smem > 48 * 1024) {
-          const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-          if (e != cudaSuccess) return e;
-        }
-        return launch_pdl(kern, dim3(row_blocks(c.N)), dim3(32 * kWarps), smem, s, static_cast<const T*>(logits), ld, p,
-                          topk_idx, weights, counts);
+        constexpr int PER = decltype(per)::value, CH = PER % 4 == 0 ? 4 : PER;
+        auto go = [&](auto kern, bool grouped_in_smem) {
+          // [E] counters, then [E] values a warp where groups are scored there: at most 4 KB + 64 KB
+          const size_t smem = ((size_t)(c.E + 1) / 2 + (grouped_in_smem ? (size_t)kWarps * c.E : 0)) * 8;
+          if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+          }
+          return launch_pdl(kern, dim3(row_blocks(c.N, fwd_blocks(PER))), dim3(32 * kWarps), smem, s,
+                            static_cast<const T*>(logits), ld, p, topk_idx, weights, counts);
+        };
+        // runs of E / 32 experts a lane: whole lanes make a group, and rows can be read in packs of CH
+        if (c.E == 32 * PER && 32 % p.groups == 0 && ld % CH == 0 && aligned_to(logits, CH * sizeof(T)))
+          return go(scores_fwd_kernel<T, PER, true>, false);
+        return go(scores_fwd_kernel<T, PER, false>, p.groups > 1);
       });
     });
   });
@@ -581,7 +696,7 @@ int moe_scores_backward(const moe_scores_config* cfg, const void* logits, int64_
       using T = decltype(tv);
       auto go = [&](auto vv) {
         const size_t smem = (size_t)kWarps * ((c.E + 3) / 4 * 4) * 4;   // at most 32 KB
-        return launch_pdl(scores_bwd_kernel<T, decltype(vv)::value>, dim3(row_blocks(c.N)), dim3(32 * kWarps), smem, s,
+        return launch_pdl(scores_bwd_kernel<T, decltype(vv)::value>, dim3(row_blocks(c.N, 8)), dim3(32 * kWarps), smem, s,
                           static_cast<const T*>(logits), ld, p, topk_idx, dweights, static_cast<T*>(dlogits), status);
       };
       if (c.E % 4 == 0 && aligned_to(dlogits, 4 * ts)) return go(std::integral_constant<int, 4>{});
