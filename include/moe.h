@@ -168,6 +168,14 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
                  const uint16_t* dY, uint16_t* dX, float* dWr, float* dWg, float* dWu, float* dWd,
                  float* dgates, void* ws, size_t ws_bytes, void* stream);
 
+/* The backward pass of the experts alone, for gates that another router made (moe_scores.h): as moe_backward
+ * without the router's part.  dX holds the expert path only; dgates (the gates' gradient, what that router's
+ * backward takes) may be NULL.  Workspace as for moe_backward. */
+int moe_experts_backward(const moe_config* cfg, const uint16_t* X, const int32_t* topk_idx, const float* gates,
+                         const uint16_t* Wg, const uint16_t* Wu, const uint16_t* Wd, const uint16_t* dY,
+                         uint16_t* dX, float* dWg, float* dWu, float* dWd, float* dgates, void* ws,
+                         size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns the first device-side error recorded in the
  * workspace's status word since the last check (MOE_OK if none), and
  * clears it. */

@@ -29,7 +29,7 @@ KERNEL_CLASSES = ["router_logits", "router_topk", "plan", "gather", "gemm_gateup
                   "distill_logits", "distill_loss", "distill_d", "distill_dx", "distill_dw"]
 
 # Every symbol include/*.h declares.
-EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "moe_forward", "moe_backward",
+EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "moe_forward", "moe_backward", "moe_experts_backward",
            "moe_check_status", "moe_set_wait_limit_ns", "moe_last_stats", "moe_strerror", "moe_profile_enable",
            "moe_profile_read", "moe_profile_reset", "moe_diag_wait_timeout", "moe_diag_gemm_wait_stats",
            "moe_route_noalloc",
@@ -119,6 +119,7 @@ def load() -> ctypes.CDLL:
             "moe_chunk_plan": [cfgp, ctypes.POINTER(I32), ctypes.POINTER(I32)],
             "moe_forward": [cfgp, P, P, P, P, P, P, P, P, SZ, P],
             "moe_backward": [cfgp, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
+            "moe_experts_backward": [cfgp, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
             "moe_check_status": [P, P],
             "moe_set_wait_limit_ns": [I64],
             "moe_last_stats": [ctypes.POINTER(MoeStats)],

@@ -14,7 +14,7 @@ import torch
 from . import _lib
 from ._lib import MoeConfig, MoeStats, check
 
-__all__ = ["Config", "workspace_bytes", "chunk_plan", "route", "plan", "forward", "backward", "check_status",
+__all__ = ["Config", "workspace_bytes", "chunk_plan", "route", "plan", "forward", "backward", "experts_backward", "check_status",
            "set_wait_limit_ns", "set_gemm_form", "set_launch_chaining", "set_dispatch", "last_stats", "profile_enable", "profile_reset", "profile_read",
            "diag_wait_timeout", "MoEBlock", "hop_rows_worst_case", "hops_workspace_bytes", "forward_hops",
            "backward_hops", "MoEHopBlock", "MoEStepGraph"]
@@ -134,6 +134,24 @@ def backward(cfg, X, Wr, topk_idx, gates, Wg, Wu, Wd, dY, dX, dWr, dWg, dWu, dWd
                                    _ptr(dWd, torch.float32, (c.E, c.H, c.I), "dWd"),
                                    _ptr(dgates, torch.float32, (c.N, c.k), "dgates"), w, n, _stream(stream)),
           "moe_backward")
+
+
+def experts_backward(cfg, X, topk_idx, gates, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, dgates, ws, stream=None) -> None:
+    c = cfg if isinstance(cfg, Config) else Config(**cfg)
+    w, n = _ws(ws)
+    check(_lib.load().moe_experts_backward(_cfg(c), _ptr(X, torch.bfloat16, (c.N, c.H), "X"),
+                                           _ptr(topk_idx, torch.int32, (c.N, c.k), "topk_idx"),
+                                           _ptr(gates, torch.float32, (c.N, c.k), "gates"),
+                                           _ptr(Wg, torch.bfloat16, (c.E, c.I, c.H), "Wg"),
+                                           _ptr(Wu, torch.bfloat16, (c.E, c.I, c.H), "Wu"),
+                                           _ptr(Wd, torch.bfloat16, (c.E, c.H, c.I), "Wd"),
+                                           _ptr(dY, torch.bfloat16, (c.N, c.H), "dY"),
+                                           _ptr(dX, torch.bfloat16, (c.N, c.H), "dX"),
+                                           _ptr(dWg, torch.float32, (c.E, c.I, c.H), "dWg"),
+                                           _ptr(dWu, torch.float32, (c.E, c.I, c.H), "dWu"),
+                                           _ptr(dWd, torch.float32, (c.E, c.H, c.I), "dWd"),
+                                           _ptr(dgates, torch.float32, (c.N, c.k), "dgates"), w, n, _stream(stream)),
+          "moe_experts_backward")
 
 
 def check_status(ws, stream=None) -> int:
@@ -276,6 +294,17 @@ class MoEBlock:
         backward(c, X, Wr, idx, gates, Wg, Wu, Wd, dY, dX, dWr, dWg, dWu, dWd, dg, self.ws, stream)
         return dict(dX=dX, dWr=dWr, dWg=dWg, dWu=dWu, dWd=dWd, dgates=dg)
 
+    def experts_backward(self, X, idx, gates, Wg, Wu, Wd, dY, stream=None):
+        """The experts' backward pass for gates of another router (ScoreRouter): no router gradient."""
+        c = self.cfg
+        dX = torch.empty_like(X)
+        dWg = torch.empty(c.E, c.I, c.H, dtype=torch.float32, device=X.device)
+        dWu = torch.empty_like(dWg)
+        dWd = torch.empty(c.E, c.H, c.I, dtype=torch.float32, device=X.device)
+        dg = torch.empty(c.N, c.k, dtype=torch.float32, device=X.device)
+        experts_backward(c, X, idx, gates, Wg, Wu, Wd, dY, dX, dWg, dWu, dWd, dg, self.ws, stream)
+        return dict(dX=dX, dWg=dWg, dWu=dWu, dWd=dWd, dgates=dg)
+
     def check(self, stream=None) -> None:
         code = check_status(self.ws, stream)
         check(code, "device status")
@@ -299,6 +328,9 @@ class MoEHopBlock(MoEBlock):
         Y = torch.empty_like(X)
         forward_hops(self.cfg, self.P, self.cap, X, idx, gates, Wg, Wu, Wd, Y, self.ws, stream)
         return Y
+
+    def experts_backward(self, X, idx, gates, Wg, Wu, Wd, dY, stream=None):
+        raise NotImplementedError("the experts' backward pass alone runs on the chunk schedule: use MoEBlock")
 
     def backward(self, X, Wr, idx, gates, Wg, Wu, Wd, dY, stream=None, want_dgates=True):
         c = self.cfg

@@ -1,5 +1,5 @@
-"""torch.autograd wrappers over the C ABI: the MoE block and the vocabulary cross-entropy head as
-differentiable functions, so they drop into a training loop.
+"""torch.autograd wrappers over the C ABI: the MoE block, the vocabulary cross-entropy head and the operators
+around them as differentiable functions, so they drop into a training loop.
 
 Argument marshalling only: forward and backward call the library's moe_route / moe_forward /
 moe_backward and moe_ce_forward / moe_ce_backward.  The library returns fp32 weight gradients;
@@ -13,8 +13,13 @@ import torch
 
 from .api import MoEBlock
 from .ce import VocabCE
+from .distill import VocabDistill
+from .embed import TokenEmbedding
+from .norm import LayerNorm
+from .scores import ScoreRouter
 
-__all__ = ["MoEFunction", "VocabCEFunction", "moe_block", "vocab_cross_entropy"]
+__all__ = ["MoEFunction", "VocabCEFunction", "moe_block", "vocab_cross_entropy", "moe_experts", "expert_scores",
+           "layer_norm", "token_embedding", "vocab_distill"]
 
 
 class MoEFunction(torch.autograd.Function):
@@ -63,3 +68,111 @@ class VocabCEFunction(torch.autograd.Function):
 def vocab_cross_entropy(X, W, targets, ce: VocabCE):
     """Differentiable mean cross-entropy head over a VocabCE's workspace."""
     return VocabCEFunction.apply(X, W, targets, ce)
+
+
+class _Experts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, idx, gates, Wg, Wu, Wd, blk):
+        ctx.blk = blk
+        ctx.save_for_backward(X, idx, gates, Wg, Wu, Wd)
+        return blk.forward(X, idx, gates, Wg, Wu, Wd)
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, idx, gates, Wg, Wu, Wd = ctx.saved_tensors
+        g = ctx.blk.experts_backward(X, idx, gates, Wg, Wu, Wd, dY.contiguous())
+        return g["dX"], None, g["dgates"], g["dWg"], g["dWu"], g["dWd"], None
+
+
+def moe_experts(X, idx, gates, Wg, Wu, Wd, blk: MoEBlock):
+    """The experts for choices and gates that another router made (expert_scores): gradients flow to X, the gates,
+    Wg, Wu and Wd."""
+    return _Experts.apply(X, idx, gates, Wg, Wu, Wd, blk)
+
+
+class _Scores(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, bias, router):
+        idx, weights, counts = router.forward(logits, bias)
+        ctx.router = router
+        ctx.save_for_backward(logits, idx)
+        ctx.mark_non_differentiable(idx, counts)
+        return idx, weights, counts
+
+    @staticmethod
+    def backward(ctx, _idx, dweights, _counts):
+        logits, idx = ctx.saved_tensors
+        return ctx.router.backward(logits, idx, dweights.contiguous()), None, None
+
+
+def expert_scores(logits, router: ScoreRouter, bias=None):
+    """(idx, weights, counts) of a ScoreRouter; the weights' gradient flows to the logits, the bias gets none."""
+    return _Scores.apply(logits, bias, router)
+
+
+def _dense_rows(t):
+    """`t` where the library can read it row by row (an expanded gradient, say, it cannot), else a copy."""
+    n, h = t.shape
+    return t if t.is_contiguous() or ((h < 2 or t.stride(1) == 1) and (n < 2 or t.stride(0) >= h)) else t.contiguous()
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, unit):
+        y, mean, rstd = unit.forward(x, weight, bias)
+        ctx.unit, ctx.bias_type = unit, None if bias is None else bias.dtype
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = ctx.unit.backward(x, weight, mean, rstd, _dense_rows(dy), want_dx=need[0],
+                                       want_dweight=need[1], want_dbias=need[2])
+        return dx, dw if dw is None else dw.to(weight.dtype), db if db is None else db.to(ctx.bias_type), None
+
+
+def layer_norm(x, weight, bias, unit: LayerNorm):
+    """Differentiable layer norm of a matrix's rows over a LayerNorm's workspace."""
+    return _LayerNorm.apply(x, weight, bias, unit)
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, unit):
+        ctx.unit, ctx.type = unit, table.dtype
+        ctx.save_for_backward(ids)
+        return unit.forward(ids, table)
+
+    @staticmethod
+    def backward(ctx, dy):
+        ids, = ctx.saved_tensors
+        return None, ctx.unit.backward(ids, _dense_rows(dy)).to(ctx.type), None
+
+
+def token_embedding(ids, table, unit: TokenEmbedding):
+    """Differentiable lookup over a TokenEmbedding's workspace (a dense gradient, in the table's type)."""
+    return _Embedding.apply(ids, table, unit)
+
+
+class _Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, ids, teacher, unit):
+        loss, lse, mean = unit.forward(X, W, ids, teacher)
+        ctx.unit = unit
+        ctx.save_for_backward(X, W, ids, teacher, lse)
+        return mean[0]
+
+    @staticmethod
+    def backward(ctx, dmean):
+        X, W, ids, teacher, lse = ctx.saved_tensors
+        n = X.shape[0]
+        dloss = (dmean.float() / max(n, 1)).expand(n).contiguous()
+        dX, dW = ctx.unit.backward(X, W, ids, teacher, lse, dloss, dW_dtype=torch.bfloat16)
+        return dX, dW, None, None, None
+
+
+def vocab_distill(X, W, ids, teacher, unit: VocabDistill):
+    """Differentiable mean distillation loss of the head X W^T against a teacher's top logits."""
+    return _Distill.apply(X, W, ids, teacher, unit)

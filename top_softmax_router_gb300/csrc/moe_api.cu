@@ -655,18 +655,25 @@ int moe_forward(const moe_config* cfg, const uint16_t* X, const int32_t* topk_id
   return MOE_OK;
 }
 
-int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, const int32_t* topk_idx,
+static int backward_checks(const moe_config* cfg, void* ws, size_t ws_bytes) {
+  const int v = validate(cfg);
+  if (v != MOE_OK) return v;
+  if (!ok_ptr(ws)) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < make_layout(*cfg).bwd_total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+// moe_backward; with Wr and dWr NULL, moe_experts_backward: the gates are given and no router follows.
+static int backward_chunks(const moe_config* cfg, const uint16_t* X, const float* Wr, const int32_t* topk_idx,
                  const float* gates, const uint16_t* Wg, const uint16_t* Wu, const uint16_t* Wd, const uint16_t* dY,
                  uint16_t* dX, float* dWr, float* dWg, float* dWu, float* dWd, float* dgates, void* ws,
                  size_t ws_bytes, void* stream) {
-  int v = validate(cfg);
+  int v = backward_checks(cfg, ws, ws_bytes);
   if (v != MOE_OK) return v;
   const moe_config& c = *cfg;
   const Layout L = make_layout(c);
-  if (!ok_ptr(ws)) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < L.bwd_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (!ok_ptr(dWr) || !ok_ptr(dWg) || !ok_ptr(dWu) || !ok_ptr(dWd)) return MOE_ERR_INVALID_ARG;
-  if (c.N > 0 && (!ok_ptr(X) || !ok_ptr(Wr) || !ok_ptr(topk_idx) || !ok_ptr(gates) || !ok_ptr(Wg) ||
+  const bool router = Wr != nullptr;
+  if ((router && !ok_ptr(dWr)) || !ok_ptr(dWg) || !ok_ptr(dWu) || !ok_ptr(dWd)) return MOE_ERR_INVALID_ARG;
+  if (c.N > 0 && (!ok_ptr(X) || (router && !ok_ptr(Wr)) || !ok_ptr(topk_idx) || !ok_ptr(gates) || !ok_ptr(Wg) ||
                   !ok_ptr(Wu) || !ok_ptr(Wd) || !ok_ptr(dY) || !ok_ptr(dX)))
     return MOE_ERR_INVALID_ARG;
   if (dgates && !aligned16(dgates)) return MOE_ERR_INVALID_ARG;
@@ -690,7 +697,7 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
     cudaError_t e = cudaMemsetAsync(dWg, 0, c.E * IH * 4, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(dWu, 0, c.E * IH * 4, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(dWd, 0, c.E * IH * 4, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dWr, 0, (size_t)c.E * c.H * 4, s);
+    if (e == cudaSuccess && dWr) e = cudaMemsetAsync(dWr, 0, (size_t)c.E * c.H * 4, s);
     if (e != cudaSuccess) return cuda_fail(e, "memset");
     set_stats(c, L, 0, L.bwd_total, L.on_load ? 1 : 2, 3);
     return MOE_OK;
@@ -703,11 +710,11 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
   if ((v = run(MOE_K_PLAN, "plan", [&] { return launch_plan(topk_idx, p, status, run.s); }))) return v;
   if ((v = run(MOE_K_PLAN, "first touch", [&] { return launch_first_touch(p, run.s); }))) return v;
   SideStream* side = nullptr;
-  {
+  if (router) {
     const cudaError_t e = side_stream(&side);
     if (e != cudaSuccess) return cuda_fail(e, "side stream");
   }
-  Launcher aux{side->s};
+  Launcher aux{router ? side->s : run.s};
   // Stream order (backward order of chunks; K-1 first):
   //   gather X(K-1) gather dY(K-1) gate/up(K-1) dActU(K-1) route grad(K-1) dWd dWg/dWu dX(K-1) gather X(K-2)
   //   unpermute(K-1) gate/up(K-2) gather dY(K-2) [router dW(K-1) forked] dActU(K-2) ...
@@ -719,6 +726,7 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
   // unpermute.  On load there are no gather kernels (the GEMMs gather their rows of X and dY themselves)
   // and dXp is the one H-wide buffer.
   auto fork_router_dw = [&](int i) -> int {
+    if (!router) return MOE_OK;
     // the side stream waits for chunk i's dlogit, then adds the chunk into dWr
     const ChunkGemm gi = chunk_gemm(c, L, p, i, status, ctr);
     cudaError_t e = cudaEventRecord(side->fork, run.s);
@@ -770,7 +778,7 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
     const bool gather_next = !L.on_load && i > 0;
     g.trigger_early = gather_next;
     if ((v = run(MOE_K_GEMM_DX, "gemm dX",
-                 [&] { return gemm_dx(g, gate, up, Wg, Wu, dl_row, Wr, dXp, run.s); })))
+                 [&] { return gemm_dx(g, gate, up, Wg, Wu, router ? dl_row : nullptr, Wr, dXp, run.s); })))
       return v;
     g.trigger_early = false;
     if (gather_next) {
@@ -785,7 +793,7 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
       return v;
   }
   if ((v = fork_router_dw(0))) return v;
-  {  // join: the caller's stream sees every router-dW update before the call's last kernel
+  if (router) {  // join: the caller's stream sees every router-dW update before the call's last kernel
     cudaError_t e = cudaEventRecord(side->join, side->s);
     if (e == cudaSuccess) e = cudaStreamWaitEvent(run.s, side->join, 0);
     if (e != cudaSuccess) return cuda_fail(e, "join side stream");
@@ -795,6 +803,30 @@ int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, cons
     return v;
   set_stats(c, L, run.launches + aux.launches, L.bwd_total, L.on_load ? 1 : 2, 3);
   return MOE_OK;
+}
+
+int moe_backward(const moe_config* cfg, const uint16_t* X, const float* Wr, const int32_t* topk_idx,
+                 const float* gates, const uint16_t* Wg, const uint16_t* Wu, const uint16_t* Wd, const uint16_t* dY,
+                 uint16_t* dX, float* dWr, float* dWg, float* dWu, float* dWd, float* dgates, void* ws,
+                 size_t ws_bytes, void* stream) {
+  if (cfg && cfg->N == 0 && !Wr && dWr) {   // no tokens: Wr is not read, and dWr is still cleared
+    static const float none = 0.0f;
+    return backward_chunks(cfg, X, &none, topk_idx, gates, Wg, Wu, Wd, dY, dX, dWr, dWg, dWu, dWd, dgates, ws,
+                           ws_bytes, stream);
+  }
+  if (!Wr) {   // the checks before a missing Wr's, then that one's answer
+    const int v = backward_checks(cfg, ws, ws_bytes);
+    return v != MOE_OK ? v : MOE_ERR_INVALID_ARG;
+  }
+  return backward_chunks(cfg, X, Wr, topk_idx, gates, Wg, Wu, Wd, dY, dX, dWr, dWg, dWu, dWd, dgates, ws, ws_bytes,
+                         stream);
+}
+
+int moe_experts_backward(const moe_config* cfg, const uint16_t* X, const int32_t* topk_idx, const float* gates,
+                         const uint16_t* Wg, const uint16_t* Wu, const uint16_t* Wd, const uint16_t* dY, uint16_t* dX,
+                         float* dWg, float* dWu, float* dWd, float* dgates, void* ws, size_t ws_bytes, void* stream) {
+  return backward_chunks(cfg, X, nullptr, topk_idx, gates, Wg, Wu, Wd, dY, dX, nullptr, dWg, dWu, dWd, dgates, ws,
+                         ws_bytes, stream);
 }
 
 int moe_hop_rows_worst_case(const moe_config* cfg, int32_t P, int32_t* rows) {

@@ -779,6 +779,7 @@ __global__ void zero_untouched_kernel(const int* __restrict__ first_touch, float
     *reinterpret_cast<float4*>(dWu + e * IH + x) = z;
     *reinterpret_cast<float4*>(dWd + e * IH + x) = z;
   }
+  if (dWr == nullptr) return;   // experts only
   for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < H; x += (int64_t)gridDim.x * blockDim.x)
     dWr[(int64_t)e * H + x] = 0.0f;
 }
