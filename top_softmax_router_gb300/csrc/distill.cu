@@ -22,9 +22,9 @@ constexpr int kGroup = 32;        // rows of a bucket
 constexpr int kHeadBand = 8;
 constexpr int kClusters = 76;     // CTA pairs of the GPU
 
-// One block a group of 32 rows, four rows a warp: q of each entry, equal classes of a row joined at the first of
+// One block a group of 32 rows, a row a warp: q of each entry, equal classes of a row joined at the first of
 // them (class[j] = -1 for every other), the row's sum of q log q, and the group's entries by class tile.
-__global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __restrict__ ids,
+__global__ void __launch_bounds__(1024) distill_prep_kernel(const int32_t* __restrict__ ids,
                                                            const float* __restrict__ teacher,
                                                            const float* __restrict__ dloss, float* __restrict__ q_out,
                                                            int32_t* __restrict__ class_out, float* __restrict__ qlogq,
@@ -33,17 +33,15 @@ __global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __rest
                                                            float T, int* status) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ int count[];            // [tiles + 1]
-  __shared__ int s_class[8][kMaxK];
-  __shared__ float s_q[8][kMaxK];
-  __shared__ int scratch[8];
+  extern __shared__ int count[];            // [tiles + 1], then each warp's classes and q [K]
+  __shared__ int scratch[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = blockIdx.x, r0 = group * kGroup;
-  for (int i = threadIdx.x; i <= tiles; i += 256) count[i] = 0;
+  const int group = blockIdx.x, r0 = group * kGroup, row = r0 + warp;
+  int* s_class = count + tiles + 1 + warp * 2 * K;
+  float* s_q = reinterpret_cast<float*>(s_class + K);
+  for (int i = threadIdx.x; i <= tiles; i += 1024) count[i] = 0;
   __syncthreads();
-  for (int k = 0; k < 4; ++k) {
-    const int row = r0 + warp * 4 + k;
-    if (row >= N) break;                    // the same for the whole warp
+  if (row < N) {                            // the same for the whole warp
     const int64_t base = (int64_t)row * K;
     float m = -INFINITY;
     for (int j = lane; j < K; j += 32) {
@@ -51,18 +49,18 @@ __global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __rest
       if (c < -1 || c >= V) report(status, MOE_ERR_DEVICE_CHECK, 711);
       const float t = teacher[base + j];
       const bool there = c >= 0 && c < V && t != -INFINITY;
-      s_class[warp][j] = there ? c : -1;
-      s_q[warp][j] = t;
+      s_class[j] = there ? c : -1;
+      s_q[j] = t;
       if (there) m = fmaxf(m, t);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float sum = 0.0f, dot = 0.0f;
     for (int j = lane; j < K; j += 32) {
-      const bool there = s_class[warp][j] >= 0;
-      const float x = there ? (s_q[warp][j] - m) / T : 0.0f;
+      const bool there = s_class[j] >= 0;
+      const float x = there ? (s_q[j] - m) / T : 0.0f;
       const float e = there ? expf(x) : 0.0f;
-      s_q[warp][j] = e;
+      s_q[j] = e;
       sum += e;
       dot = fmaf(e, x, dot);
     }
@@ -75,13 +73,13 @@ __global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __rest
     }
     __syncwarp();
     for (int j = lane; j < K; j += 32) {
-      int c = s_class[warp][j];
+      int c = s_class[j];
       float q = 0.0f;
       if (c >= 0) {
         bool first = true;
-        for (int i = 0; i < j; ++i) first &= s_class[warp][i] != c;
+        for (int i = 0; i < j; ++i) first &= s_class[i] != c;
         if (first)
-          for (int i = j; i < K; ++i) q += s_class[warp][i] == c ? s_q[warp][i] : 0.0f;
+          for (int i = j; i < K; ++i) q += s_class[i] == c ? s_q[i] : 0.0f;
         else
           c = -1;
       }
@@ -93,7 +91,7 @@ __global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __rest
   }
   __syncthreads();
   // exclusive scan of the counts; thread t owns a run of tiles
-  const int per = (tiles + 255) / 256, t0 = threadIdx.x * per, t1 = min(tiles, t0 + per);
+  const int per = (tiles + 1023) / 1024, t0 = threadIdx.x * per, t1 = min(tiles, t0 + per);
   int own = 0;
   for (int t = t0; t < t1; ++t) own += count[t];
   int x = own;
@@ -117,12 +115,10 @@ __global__ void __launch_bounds__(256) distill_prep_kernel(const int32_t* __rest
   if (t0 < tiles && t1 == tiles) b[tiles] = at;
   __syncthreads();
   // an entry's place within its bucket does not change any result
-  for (int k = 0; k < 4; ++k) {
-    const int row = r0 + warp * 4 + k;
-    if (row >= N) break;
+  if (row < N) {
     for (int j = lane; j < K; j += 32) {
-      const int c = class_out[(int64_t)row * K + j];
-      if (c >= 0) entry[atomicAdd(count + (c >> 8), 1)] = (uint32_t)(row - r0) | (uint32_t)(c & 255) << 5 | (uint32_t)j << 13;
+      const int c = class_out[(int64_t)row * K + j];   // this lane's own
+      if (c >= 0) entry[atomicAdd(count + (c >> 8), 1)] = (uint32_t)warp | (uint32_t)(c & 255) << 5 | (uint32_t)j << 13;
     }
   }
 }
@@ -279,8 +275,12 @@ bool ok4(const void* p) { return p != nullptr && aligned_to(p, 4); }
 int prepare(const moe_distill_config& c, const DistillLayout& L, const int32_t* ids, const float* teacher,
             const float* dloss, uint8_t* w, cudaStream_t s) {
   return timed_launch(MOE_K_DISTILL_PREP, "distill entries", s, [&] {
-    const size_t smem = (size_t)(L.tiles + 1) * 4;   // at most 16 KB
-    return launch_pdl(distill_prep_kernel, dim3(L.groups), dim3(256), smem, s, ids, teacher, dloss,
+    const size_t smem = (size_t)(L.tiles + 1 + kGroup * 2 * c.K) * 4;   // at most 16 + 64 KB
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(distill_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(distill_prep_kernel, dim3(L.groups), dim3(1024), smem, s, ids, teacher, dloss,
                       reinterpret_cast<float*>(w + L.q), reinterpret_cast<int32_t*>(w + L.cls),
                       reinterpret_cast<float*>(w + L.qlogq),
                       dloss ? reinterpret_cast<float*>(w + L.coef) : static_cast<float*>(nullptr),
@@ -340,6 +340,7 @@ int moe_distill_forward(const moe_distill_config* cfg, const uint16_t* X, const 
     p.M = c.N;
     p.N = c.V;
     p.nk = c.H / GEMM_BK;
+    p.share = kLseShare;
     p.part_m = reinterpret_cast<float*>(w + L.part_m);
     p.part_z = reinterpret_cast<float*>(w + L.part_z);
     p.entry_logit = reinterpret_cast<float*>(w + L.entry_logit);

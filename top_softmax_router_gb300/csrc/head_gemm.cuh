@@ -29,6 +29,7 @@ struct HeadGemm {
   int splits;                // HEAD_OUT: shares of K, each with its own output (1: no split)
   int* status;
   int64_t limit_ns;
+  int share;                 // HEAD_LSE: K blocks that one accumulator sums (see kLseShare)
   // HEAD_LSE, HEAD_D
   float to_log2;             // log2(e) / T: logits in units of T ln 2
   int tile0;                 // class tile (of 256) of column 0
@@ -49,6 +50,13 @@ struct HeadGemm {
   uint16_t* out16;           // [M][ldo] or NULL
   int ldo;
 };
+
+// The tensor cores cut each addition to an accumulator off towards zero, so that a logit of H products comes out too
+// small, by up to H / 16 x 2^-24 of itself, the larger the logit the more, and lse with it (H = 4096: 1.5e-6 of lse,
+// against 5e-8 of fp32 sums).  The forward therefore sums 1024 products to an accumulator and adds those in fp32
+// registers: the accumulators stay small, and so does what is cut off (3.6e-7; 512 products: 1.7e-7, but the forward of
+// 8192 x 4096 x 65536 took 2903 us for 2689; unsplit 2579).  d is rounded to bf16 and is left alone.
+constexpr int kLseShare = 16;
 
 struct HeadSmem {
   static constexpr int HALF = 128 * GEMM_BK * 2;       // 16 KB: this CTA's rows of A, or its half of B
@@ -74,6 +82,35 @@ __device__ __forceinline__ float tc_ld1(uint32_t taddr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   return __uint_as_float(r);
+}
+
+// v[j] += this thread's lane of 16 consecutive fp32 columns of tensor memory.
+__device__ __forceinline__ void tc_add16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
+}
+
+// 32 lanes x 32 consecutive fp32 columns of tensor memory from the threads' values.
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 
 // The epilogue of one warp: rows row0 + lane (valid below p.M), the columns c0 .. c0 + 127 of column tile nt.  none: the
@@ -123,14 +160,18 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
     if (row0 < p.M) {
       const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
       const int e1 = b[1];
-      for (int e = b[0]; e < e1; ++e) {
-        const uint32_t rec = p.entry[e];
-        const int c = (rec >> 5) & 255;
-        if ((c >> 7) != half) continue;               // the same for the whole warp
-        const float y = tc_ld1(tacc + c);
-        if (ok && lane == (int)(rec & 31))             // this thread wrote the element above
-          d[c] = __bfloat16_as_ushort(__float2bfloat16_rn(
-              coef * (exp2_fast(fmaf(y, p.to_log2, -l)) - p.q[(int64_t)row * p.K + (rec >> 13)])));
+      for (int e0 = b[0]; e0 < e1; e0 += 32) {        // 32 records (and their q) a load
+        const uint32_t recs = e0 + lane < e1 ? p.entry[e0 + lane] : 0;
+        const float qs = e0 + lane < e1 ? p.q[(int64_t)(row0 + (int)(recs & 31)) * p.K + (recs >> 13)] : 0.0f;
+        const int n = min(32, e1 - e0);
+        for (int i = 0; i < n; ++i) {
+          const uint32_t rec = __shfl_sync(0xffffffffu, recs, i);
+          const int c = (rec >> 5) & 255;
+          if ((c >> 7) != half) continue;             // the same for the whole warp
+          const float q = __shfl_sync(0xffffffffu, qs, i), y = tc_ld1(tacc + c);
+          if (ok && lane == (int)(rec & 31))           // this thread wrote the element above
+            d[c] = __bfloat16_as_ushort(__float2bfloat16_rn(coef * (exp2_fast(fmaf(y, p.to_log2, -l)) - q)));
+        }
       }
     }
   } else {
@@ -163,12 +204,16 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
     if (row0 < p.M) {
       const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
       const int e1 = b[1];
-      for (int e = b[0]; e < e1; ++e) {
-        const uint32_t rec = p.entry[e];
-        const int c = (rec >> 5) & 255;
-        if ((c >> 7) != half) continue;
-        const float y = tc_ld1(tacc + c);
-        if (ok && lane == (int)(rec & 31)) p.entry_logit[(int64_t)row * p.K + (rec >> 13)] = y;
+      for (int e0 = b[0]; e0 < e1; e0 += 32) {
+        const uint32_t recs = e0 + lane < e1 ? p.entry[e0 + lane] : 0;
+        const int n = min(32, e1 - e0);
+        for (int i = 0; i < n; ++i) {
+          const uint32_t rec = __shfl_sync(0xffffffffu, recs, i);
+          const int c = (rec >> 5) & 255;
+          if ((c >> 7) != half) continue;
+          const float y = tc_ld1(tacc + c);
+          if (ok && lane == (int)(rec & 31)) p.entry_logit[(int64_t)row * p.K + (rec >> 13)] = y;
+        }
       }
     }
   }
@@ -291,39 +336,46 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int w = cluster; w < total && ok; w += clusters, ++it) {
-        const int acc = it & 1;
-        int good = 1;
-        if (lane == 0)
-          good = wait_bounded(tempty_bar(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.limit_ns, p.status, 702);
-        if (!__shfl_sync(0xffffffffu, good, 0)) break;
-        tc_fence_after();
-        const uint32_t tacc = tmem_base + acc * 256;
+      for (int w = cluster; w < total && ok; w += clusters) {
         int mt, nt, kb0, kb1, split;
         head_tile(p, w, &mt, &nt, &kb0, &kb1, &split);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (lane == 0) good = wait_bounded(full_bar(stage), phase, abort_flag, p.limit_ns, p.status, 703);
+        const int step = EPI == HEAD_LSE ? p.share : max(1, kb1 - kb0);
+        // one accumulator after the other (an empty share of K still passes its accumulator on)
+        for (int k0 = kb0; ok && (k0 < kb1 || k0 == kb0); k0 += step, ++it) {
+          const int acc = it & 1;
+          int good = 1;
+          if (lane == 0)
+            good = wait_bounded(tempty_bar(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.limit_ns, p.status, 702);
           if (!__shfl_sync(0xffffffffu, good, 0)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = sbase + stage * S::STAGE, sb = sa + S::HALF;
-          if (lane == 0) {
-#pragma unroll
-            for (int kk = 0; kk < GEMM_BK / 16; ++kk) {
-              const uint64_t ad = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024) : smem_desc_sw128(sa + kk * 32, 0, 1024);
-              const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 0, 1024);
-              tc_mma_pair(tacc, ad, bd, idesc, kb != kb0 || kk != 0 ? 1u : 0u);
+          const uint32_t tacc = tmem_base + acc * 256;
+          for (int kb = k0; kb < min(kb1, k0 + step); ++kb) {
+            if (lane == 0) good = wait_bounded(full_bar(stage), phase, abort_flag, p.limit_ns, p.status, 703);
+            if (!__shfl_sync(0xffffffffu, good, 0)) {
+              ok = false;
+              break;
             }
-            tc_commit_pair(empty_bar(stage), 0x3);
+            tc_fence_after();
+            const uint32_t sa = sbase + stage * S::STAGE, sb = sa + S::HALF;
+            if (lane == 0) {
+#pragma unroll
+              for (int kk = 0; kk < GEMM_BK / 16; ++kk) {
+                const uint64_t ad = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024) : smem_desc_sw128(sa + kk * 32, 0, 1024);
+                const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 0, 1024);
+                tc_mma_pair(tacc, ad, bd, idesc, kb != k0 || kk != 0 ? 1u : 0u);
+              }
+              tc_commit_pair(empty_bar(stage), 0x3);
+            }
+            __syncwarp();
+            if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
           }
+          if (!ok) break;
+          if (lane == 0) tc_commit_pair(tfull_bar(acc), 0x3);
           __syncwarp();
-          if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (!ok) break;
-        if (lane == 0) tc_commit_pair(tfull_bar(acc), 0x3);
-        __syncwarp();
       }
       if (lane == 0) {                              // every MMA has completed before the tensor memory is freed
         tc_commit_pair(drain_bar, 0x1);
@@ -336,21 +388,45 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, half = (warp - 2) >> 2;   // the quarter of the lanes this warp may read
     int it = 0;
-    for (int w = cluster; w < total; w += clusters, ++it) {
-      const int acc = it & 1;
-      int good = 1;
-      if (lane == 0) good = wait_bounded(tfull_bar(acc), (it >> 1) & 1, abort_flag, p.limit_ns, p.status, 704);
-      if (!__shfl_sync(0xffffffffu, good, 0)) break;
-      tc_fence_after();
+    bool ok = true;
+    for (int w = cluster; w < total && ok; w += clusters) {
       int mt, nt, kb0, kb1, split;
       head_tile(p, w, &mt, &nt, &kb0, &kb1, &split);
-      head_epilogue<EPI>(p, mt * 256 + 128 * (int)rank + q * 32, nt, half, split, kb0 == kb1,
-                         tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256, lane);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(tempty_bar(acc));
-        else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+      const int accs = EPI == HEAD_LSE ? (p.nk + p.share - 1) / p.share : 1;
+      float sum[EPI == HEAD_LSE ? 128 : 1];   // of the accumulators so far
+      if constexpr (EPI == HEAD_LSE) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+      }
+      for (int a = 0; a < accs; ++a, ++it) {
+        const int acc = it & 1;
+        int good = 1;
+        if (lane == 0) good = wait_bounded(tfull_bar(acc), (it >> 1) & 1, abort_flag, p.limit_ns, p.status, 704);
+        if (!__shfl_sync(0xffffffffu, good, 0)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 256;
+        if constexpr (EPI == HEAD_LSE) {
+          if (accs > 1) {
+#pragma unroll
+            for (int c = 0; c < 128; c += 16) tc_add16(tacc + half * 128 + c, sum + c);
+            if (a + 1 == accs) {   // the sums take the last accumulator's place
+#pragma unroll
+              for (int c = 0; c < 128; c += 32) tc_st32(tacc + half * 128 + c, sum + c);
+              asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            }
+          }
+        }
+        if (a + 1 == accs)
+          head_epilogue<EPI>(p, mt * 256 + 128 * (int)rank + q * 32, nt, half, split, kb0 == kb1, tacc, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(tempty_bar(acc));
+          else mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+        }
       }
     }
   }
