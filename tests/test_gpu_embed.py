@@ -89,6 +89,20 @@ def test_the_sum_does_not_depend_on_how_many_tokens_surround_it(M):
         assert torch.equal(emb.backward(ids.cuda(), dy).double(), ref)
 
 
+@pytest.mark.parametrize("n,v,h", [(65536, 900, 4), (65537, 400, 8), (66000, 1, 4), (150000, 70000, 4), (70001, 600000, 1)])
+def test_many_tokens(M, n, v, h):
+    """The sort's last length in one cluster, and beyond it; integers, so that every order of the sums is exact."""
+    ids, _, _ = make(n, v, 1, "fp32", seed=n, hot=0.1)
+    ids[::5000] = -1 if n % 2 else v
+    dy = torch.randint(-4, 5, (n, h), generator=torch.Generator().manual_seed(n)).float().cuda()
+    emb = M.TokenEmbedding(M.EmbeddingConfig(N=n, V=v, H=h))
+    ok = (ids >= 0) & (ids < v)
+    ref = torch.zeros(v, h, dtype=torch.float64, device="cuda").index_add_(0, ids[ok].cuda(), dy[ok.cuda()].double())
+    assert torch.equal(emb.backward(ids.cuda(), dy).double(), ref)
+    base = torch.ones(v, h, device="cuda")
+    assert torch.equal(emb.backward(ids.cuda(), dy, into=base).double(), ref + 1)
+
+
 def test_padding_id_has_no_gradient(M):
     ids, table, dy = (t.cuda() for t in make(500, 20, 16, "bf16", seed=2))
     emb = M.TokenEmbedding(M.EmbeddingConfig(N=500, V=20, H=16, padding_idx=7))

@@ -193,12 +193,16 @@ __global__ void __launch_bounds__(kSortThreads, 1)
     __syncwarp();
     cluster_sync();
     int all = 0, ahead = 0;
-    if ((int)threadIdx.x < bins)
-      for (int c = 0; c < blocks; ++c) {
-        const int v = load_cluster(mapa_shared(total_addr + 4 * threadIdx.x, c));
-        all += v;
-        if (c < rank) ahead += v;
+    if ((int)threadIdx.x < bins) {
+      int v[kCluster];   // all on their way before the first is waited for
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) v[c] = c < blocks ? load_cluster(mapa_shared(total_addr + 4 * threadIdx.x, c)) : 0;
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        all += v[c];
+        if (c < rank) ahead += v[c];
       }
+    }
     const int before = exclusive_scan(all, scratch);
     warp_places(cnt, bins, before + ahead);
     __syncthreads();
@@ -330,29 +334,50 @@ __device__ __forceinline__ int lower_bound_warp(const uint32_t* keys, int n, uin
   return lo;
 }
 
-// a[j] += sum over sorted places [s, e) of dy[order[place]][c + j], in order, eight rows' loads at a time.
-template <class T, int VEC>
-__device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy, const int* __restrict__ order, int s,
-                                         int e, int c, float (&a)[VEC]) {
-  int i = s;
-  for (; i + 8 <= e; i += 8) {
-    Pack<T, VEC> p[8];
+// a[k][j] += sum over i < n of dy[order[i]][c + k step + j], in order, eight rows' loads at a time.
+// PACKS (1 or 2) packs a thread sums at a time, `step` columns apart.
+template <int PACKS, class T, int VEC>
+__device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy, const int* order, int n, int c, int step,
+                                         int H, float (&a)[PACKS][VEC]) {
+  const bool more = PACKS > 1 && c + step < H;
+  int i = 0;
+  for (; i + 8 <= n; i += 8) {
+    Pack<T, VEC> p[8][PACKS];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] = load_pack<T, VEC>(dy + order[i + k] * lddy + c);
+    for (int r = 0; r < 8; ++r) {
+      const T* row = dy + order[i + r] * lddy + c;
+      p[r][0] = load_pack<T, VEC>(row);
+      if constexpr (PACKS > 1) {
+        p[r][1] = zero_pack<T, VEC>();
+        if (more) p[r][1] = load_pack<T, VEC>(row + step);
+      }
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int k = 0; k < PACKS; ++k) {
+        float f[VEC];
+        unpack<T, VEC>(p[r][k], f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[k][j] += f[j];
+      }
+  }
+#pragma unroll 4
+  for (; i < n; ++i) {
+    const T* row = dy + order[i] * lddy + c;
+    Pack<T, VEC> p[PACKS];
+    p[0] = load_pack<T, VEC>(row);
+    if constexpr (PACKS > 1) {
+      p[1] = zero_pack<T, VEC>();
+      if (more) p[1] = load_pack<T, VEC>(row + step);
+    }
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
       float f[VEC];
       unpack<T, VEC>(p[k], f);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a[j] += f[j];
+      for (int j = 0; j < VEC; ++j) a[k][j] += f[j];
     }
-  }
-  for (; i < e; ++i) {
-    const Pack<T, VEC> p = load_pack<T, VEC>(dy + order[i] * lddy + c);
-    float f[VEC];
-    unpack<T, VEC>(p, f);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) a[j] += f[j];
   }
 }
 
@@ -366,12 +391,15 @@ __global__ void __launch_bounds__(256) embed_piece_kernel(const uint32_t* __rest
   pdl_wait();
   pdl_trigger();
   __shared__ int edge[4];   // run of the first place: start, end; run of the last place: start, end
+  __shared__ int places[kPiece];
   const int p0 = blockIdx.x * kPiece, p1 = min(N, p0 + kPiece);
   const int warp = threadIdx.x >> 5;
   if (warp < 4) {
     const uint32_t v = keys[warp < 2 ? p0 : p1 - 1];
     const int at = v >= (uint32_t)V ? 0 : lower_bound_warp(keys, N, v + (warp & 1));
     if ((threadIdx.x & 31) == 0) edge[warp] = at;
+  } else if ((int)threadIdx.x - 128 < p1 - p0) {
+    places[threadIdx.x - 128] = order[p0 + threadIdx.x - 128];
   }
   __syncthreads();
   const int s0 = edge[0], e0 = edge[1], s1 = edge[2], e1 = edge[3];
@@ -381,22 +409,67 @@ __global__ void __launch_bounds__(256) embed_piece_kernel(const uint32_t* __rest
     const int a0 = max(s, p0), a1 = min(e, p1);
     float* out = part + ((int64_t)blockIdx.x * 2 + which) * H;
     for (int c = (blockIdx.y * 256 + threadIdx.x) * VEC; c < H; c += gridDim.y * 256 * VEC) {
-      float a[VEC];
+      float a[1][VEC];
       Pack<float, VEC> o;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a[j] = 0.0f;
-      add_rows<T, VEC>(dy, lddy, order, a0, a1, c, a);
+      for (int j = 0; j < VEC; ++j) a[0][j] = 0.0f;
+      add_rows<1, T, VEC>(dy, lddy, places + (a0 - p0), a1 - a0, c, 0, H, a);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o.v[j] = a[j];
+      for (int j = 0; j < VEC; ++j) o.v[j] = a[0][j];
       store_pack<float, VEC>(out + c, o);
     }
   }
 }
 
-// Block b owns table rows [R b, R (b + 1)), `tpr` threads (a power of two) a row; thread t of a row takes the packs
-// t, t + tpr, ..  Four floats a pack: a warp's store is one run of 512 bytes.
-template <class T, int VEC, bool ADD>
-__global__ void __launch_bounds__(256) embed_rows_kernel(const uint32_t* __restrict__ keys,
+// The row of run [s, e): its sum (of the tokens in `order`, from s on, or of its pieces), scaled and stored or added.
+// `tpr` threads; thread t takes the packs t, t + tpr, .., PACKS at a time.  Four floats a pack: a warp's store is one
+// run of 512 bytes.
+template <int PACKS, bool ADD, class T, int VEC>
+__device__ __forceinline__ void embed_row(const int* order, const T* __restrict__ dy, int64_t lddy,
+                                          const float* __restrict__ part, float* __restrict__ row, int s, int e, int H,
+                                          int t, int tpr, float scale) {
+  const int step = tpr * VEC;
+  for (int c = t * VEC; c < H; c += PACKS * step) {
+    Pack<float, VEC> o[PACKS];
+    float a[PACKS][VEC];
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+      if (ADD && c + k * step < H) o[k] = load_pack<float, VEC>(row + c + k * step);   // while the tokens are summed
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) a[k][j] = 0.0f;
+    }
+    if (e - s <= kPiece) {
+      add_rows<PACKS, T, VEC>(dy, lddy, order, e - s, c, step, H, a);
+    } else {
+#pragma unroll 4
+      for (int b = s / kPiece; b <= (e - 1) / kPiece; ++b) {
+        const float* from = part + ((int64_t)b * 2 + (b * kPiece < s ? 1 : 0)) * H + c;
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k)
+          if (k == 0 || c + k * step < H) {
+            const Pack<float, VEC> p = load_pack<float, VEC>(from + k * step);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) a[k][j] += p.v[j];
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+      if (k > 0 && c + k * step >= H) break;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[k].v[j] = ADD ? fmaf(scale, a[k][j], o[k].v[j]) : scale * a[k][j];
+      if constexpr (VEC == 4) {   // written once and not read again here: first to leave L2
+        __stcs(reinterpret_cast<float4*>(row + c + k * step), make_float4(o[k].v[0], o[k].v[1], o[k].v[2], o[k].v[3]));
+      } else {
+        store_pack<float, VEC>(row + c + k * step, o[k]);
+      }
+    }
+  }
+}
+
+// A dense gradient: block b owns table rows [R b, R (b + 1)).
+template <class T, int VEC>
+__global__ void __launch_bounds__(256, 4) embed_rows_kernel(const uint32_t* __restrict__ keys,
                                                         const int* __restrict__ order, const T* __restrict__ dy,
                                                         int64_t lddy, const float* __restrict__ part,
                                                         float* __restrict__ dW, int N, int V, int H, int R, int tpr,
@@ -413,43 +486,55 @@ __global__ void __launch_bounds__(256) embed_rows_kernel(const uint32_t* __restr
   }
   __syncthreads();
   const int lo = first[0], hi = first[rows];
-  if (ADD && lo == hi) return;
   if (threadIdx.x > 0 && (int)threadIdx.x < rows) first[threadIdx.x] = lower_bound(keys, lo, hi, (uint32_t)(v0 + threadIdx.x));
   __syncthreads();
-  const int t = threadIdx.x & (tpr - 1);
-  for (int r = threadIdx.x / tpr; r < rows; r += 256 / tpr) {
-    const int s = first[r], e = first[r + 1];
-    if (ADD && s == e) continue;
-    float* row = dW + (v0 + r) * H;
-    for (int c = t * VEC; c < H; c += tpr * VEC) {
-      Pack<float, VEC> o;
-      float a[VEC];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) a[j] = 0.0f;
-      if (e - s <= kPiece) {
-        add_rows<T, VEC>(dy, lddy, order, s, e, c, a);
-      } else {
-        for (int b = s / kPiece; b <= (e - 1) / kPiece; ++b) {
-          const Pack<float, VEC> p = load_pack<float, VEC>(part + ((int64_t)b * 2 + (b * kPiece < s ? 1 : 0)) * H + c);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) a[j] += p.v[j];
-        }
-      }
-      if (ADD) {
-        o = load_pack<float, VEC>(row + c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o.v[j] = fmaf(scale, a[j], o.v[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o.v[j] = scale * a[j];
-      }
-      if constexpr (VEC == 4) {   // written once and not read again here: first to leave L2
-        __stcs(reinterpret_cast<float4*>(row + c), make_float4(o.v[0], o.v[1], o.v[2], o.v[3]));
-      } else {
-        store_pack<float, VEC>(row + c, o);
-      }
+  for (int r = threadIdx.x / tpr; r < rows; r += 256 / tpr)
+    embed_row<1, false, T, VEC>(order + first[r], dy, lddy, part, dW + (v0 + r) * H, first[r], first[r + 1], H, threadIdx.x & (tpr - 1),
+                             tpr, scale);
+}
+
+// Added into a gradient: only rows of tokens that occur.  Block b takes the runs that start at the sorted places
+// [kHeads b, kHeads (b + 1)), which it sees by itself (searching for its rows as the dense form does cost twice the
+// time: 52 us for 16384 tokens of 2048 columns).
+constexpr int kHeads = 8;
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) embed_add_kernel(const uint32_t* __restrict__ keys,
+                                                       const int* __restrict__ order, const T* __restrict__ dy,
+                                                       int64_t lddy, const float* __restrict__ part,
+                                                       float* __restrict__ dW, int N, int V, int H, int tpr,
+                                                       float scale) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int run_s[kHeads], run_e[kHeads], run_v[kHeads], runs;
+  __shared__ int places[kHeads][kPiece];
+  const int p0 = blockIdx.x * kHeads;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, p = p0 + lane;
+    const uint32_t v = p < N ? keys[p] : 0xFFFFFFFFu;
+    uint32_t before = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) before = p > 0 ? keys[p - 1] : 0xFFFFFFFEu;
+    const bool head = v != before;                             // the place past the last is one too
+    const uint32_t heads = __ballot_sync(0xffffffffu, head);
+    const bool mine = head && lane < kHeads && v < (uint32_t)V;
+    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+    if (mine) {
+      const uint32_t after = lane == 31 ? 0u : heads >> (lane + 1);
+      const int i = __popc(all & ((1u << lane) - 1u));
+      run_s[i] = p;
+      run_e[i] = after ? p + __ffs(after) : lower_bound(keys, min(N, p0 + 32), N, v + 1);
+      run_v[i] = (int)v;
     }
+    if (lane == 0) runs = __popc(all);
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < runs * kPiece; i += 256) {
+    const int r = i / kPiece, k = i % kPiece;
+    if (run_s[r] + k < run_e[r]) places[r][k] = order[run_s[r] + k];
+  }
+  __syncthreads();
+  for (int r = threadIdx.x / tpr; r < runs; r += 256 / tpr)
+    embed_row<2, true, T, VEC>(places[r], dy, lddy, part, dW + (int64_t)run_v[r] * H, run_s[r], run_e[r], H,
+                            threadIdx.x & (tpr - 1), tpr, scale);
 }
 
 struct EmbedLayout {
@@ -645,11 +730,11 @@ int moe_embed_backward(const moe_embed_config* cfg, const void* ids, int32_t id_
         const int R = (int)std::min<int64_t>(256, std::max<int64_t>(1, 32768 / c.H));
         const dim3 grid((unsigned)(((int64_t)c.V + R - 1) / R));
         int tpr = 1;
-        while (tpr < 256 && tpr * VEC < c.H) tpr *= 2;
+        while (tpr < 256 && tpr * VEC * (accumulate ? 2 : 1) < c.H) tpr *= 2;   // packs a thread: two at a time, or one
         if (accumulate)
-          return launch_pdl(embed_rows_kernel<T, VEC, true>, grid, dim3(256), 0, s, keys, order, g, lddy,
-                            static_cast<const float*>(part), dW, c.N, c.V, c.H, R, tpr, c.scale);
-        return launch_pdl(embed_rows_kernel<T, VEC, false>, grid, dim3(256), 0, s, keys, order, g, lddy,
+          return launch_pdl(embed_add_kernel<T, VEC>, dim3((c.N + kHeads - 1) / kHeads), dim3(256), 0, s, keys, order, g,
+                            lddy, static_cast<const float*>(part), dW, c.N, c.V, c.H, tpr, c.scale);
+        return launch_pdl(embed_rows_kernel<T, VEC>, grid, dim3(256), 0, s, keys, order, g, lddy,
                           static_cast<const float*>(part), dW, c.N, c.V, c.H, R, tpr, c.scale);
       };
       if (c.H % 4 == 0 && lddy % 4 == 0 && aligned_to(dy, 4 * ts) && aligned_to(dW, 16))

@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float* __restric
   float a = 0.0f;
   if (c < H) {
     const float* p = part + (second ? H : 0) + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int b = warp; b < blocks; b += 32) a += p[(int64_t)b * 2 * H];
   }
   s[lane][warp] = a;

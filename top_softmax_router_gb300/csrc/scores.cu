@@ -490,10 +490,11 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
     }
   }
   if (counts) {
-    // integer adds: the order does not change the result
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 32 * kWarps)
-      if (hist[e]) atomicAdd(counts + e, hist[e]);
+    for (int e = threadIdx.x; e < E; e += 32 * kWarps) {
+      if (gridDim.x == 1) counts[e] = hist[e];
+      else if (hist[e]) atomicAdd(counts + e, hist[e]);   // integer adds: the order does not change the result
+    }
   }
 }
 
@@ -645,7 +646,7 @@ int moe_scores_forward(const moe_scores_config* cfg, const void* logits, int64_t
   if (c.N > 0 && (!logits || !topk_idx || !weights || !aligned_to(logits, type_size(type)) ||
                   !aligned_to(topk_idx, 4) || !aligned_to(weights, 4)))
     return MOE_ERR_INVALID_ARG;
-  if (counts) {
+  if (counts && (c.N == 0 || c.N > kWarps)) {   // a single block stores them
     const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)c.E * 4, s);
     if (e != cudaSuccess) return record_cuda_error(e, "clear counts");
   }
