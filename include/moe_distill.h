@@ -8,7 +8,8 @@
  *              teacher logit t[n, j]), K at most; the student's softmax runs over all V classes
  *   loss[n]  = T^2 sum_j q[n, j] (log q[n, j] - z[n, id[n, j]] + lse[n])       (KL, scaled by T^2)
  *   and, for an upstream gradient g[n] of loss[n],
- *   d[n, v]  = g[n] T (exp(z[n, v] - lse[n]) - sum over j with id[n, j] = v of q[n, j])   (stored in bf16)
+ *   d[n, v]  = g[n] T (exp(z[n, v] - lse[n]) - sum over j with id[n, j] = v of q[n, j])   (stored in bf16,
+ *              relative to g[0] T)
  *   dX[n]    = sum_v d[n, v] W[v]    (fp32 accumulation, stored bf16)
  *   dW[v]    = sum_n d[n, v] X[n]    (fp32 accumulation, stored bf16 or fp32)
  *

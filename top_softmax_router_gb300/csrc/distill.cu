@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(1024) distill_prep_kernel(const int32_t* __res
                                                            const float* __restrict__ teacher,
                                                            const float* __restrict__ dloss, float* __restrict__ q_out,
                                                            int32_t* __restrict__ class_out, float* __restrict__ qlogq,
-                                                           float* __restrict__ coef, int* __restrict__ bucket,
+                                                           float* __restrict__ coef, float* __restrict__ out_scale,
+                                                           int* __restrict__ bucket,
                                                            uint32_t* __restrict__ entry, int N, int V, int K, int tiles,
                                                            float T, int* status) {
   pdl_wait();
@@ -69,7 +70,13 @@ __global__ void __launch_bounds__(1024) distill_prep_kernel(const int32_t* __res
     const bool some = sum != 0.0f;          // the largest entry's e is 1
     if (lane == 0) {
       qlogq[row] = some ? dot / sum - logf(sum) : 0.0f;
-      if (coef) coef[row] = some ? dloss[row] * T : 0.0f;
+      if (coef) {
+        // d is stored relative to the first row's gradient, which the products' epilogues put back in fp32: with one
+        // gradient for all rows (a mean) its rounding would otherwise be the same in every d and not average out
+        const float g0 = dloss[0], c = fabsf(g0) >= 0x1p-30f && fabsf(g0) <= 0x1p30f ? g0 : 1.0f;
+        coef[row] = some ? dloss[row] / c : 0.0f;
+        if (row == 0) *out_scale = c * T;
+      }
     }
     __syncwarp();
     for (int j = lane; j < K; j += 32) {
@@ -214,7 +221,7 @@ struct DistillLayout {
   int groups, tiles;     // groups of 32 rows; class tiles of 256
   int Vs, S;             // classes a strip (a multiple of 256), strips
   int splits;            // shares of a strip's classes in the dX GEMM
-  size_t q, cls, qlogq, coef, bucket, entry;
+  size_t q, cls, qlogq, coef, out_scale, bucket, entry;
   size_t part_m, part_z, entry_logit, fwd_total;
   size_t d, acc, bwd_total;
 };
@@ -241,6 +248,7 @@ DistillLayout distill_layout(const moe_distill_config& c) {
   L.cls = take((size_t)N * K * 4);
   L.qlogq = take((size_t)N * 4);
   L.coef = take((size_t)N * 4);
+  L.out_scale = take(4);
   L.bucket = take((size_t)L.groups * (L.tiles + 1) * 4);
   L.entry = take((size_t)L.groups * kGroup * K * 4);
   const size_t common = o;
@@ -284,6 +292,7 @@ int prepare(const moe_distill_config& c, const DistillLayout& L, const int32_t* 
                       reinterpret_cast<float*>(w + L.q), reinterpret_cast<int32_t*>(w + L.cls),
                       reinterpret_cast<float*>(w + L.qlogq),
                       dloss ? reinterpret_cast<float*>(w + L.coef) : static_cast<float*>(nullptr),
+                      reinterpret_cast<float*>(w + L.out_scale),
                       reinterpret_cast<int*>(w + L.bucket), reinterpret_cast<uint32_t*>(w + L.entry), c.N, c.V, c.K,
                       L.tiles, c.temperature, reinterpret_cast<int*>(w));
   });
@@ -300,6 +309,7 @@ HeadGemm head_params(const moe_distill_config& c, const DistillLayout& L, uint8_
   p.bucket = reinterpret_cast<const int*>(w + L.bucket);
   p.entry = reinterpret_cast<const uint32_t*>(w + L.entry);
   p.q = reinterpret_cast<const float*>(w + L.q);
+  p.out_scale = reinterpret_cast<const float*>(w + L.out_scale);
   return p;
 }
 

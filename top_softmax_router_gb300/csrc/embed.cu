@@ -24,8 +24,11 @@ constexpr int kCluster = 8;          // blocks that sort together through distri
 constexpr int kMaxBits = 9;          // bits of a digit: kSortWarps x 512 counters are 64 KB
 
 // ---------------------------------------------------------------------------
-// Forward: one warp a 16 x 32-byte piece of a row, so a short batch still spreads over the SMs.
+// Forward: a warp copies a piece of up to 32 x PER packs of a row, so that a short batch still spreads over the SMs: four
+// packs of 16 bytes a lane, or 16 single elements where rows do not start on 16 bytes.
 // ---------------------------------------------------------------------------
+template <int VEC>
+constexpr int kFwdPer = VEC == 1 ? 16 : 4;
 template <class T, class I, int VEC>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const I* __restrict__ ids, const T* __restrict__ table,
                                                        T* __restrict__ y, int N, int V, int H, int pieces,
@@ -35,21 +38,22 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const I* __restrict__ id
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t n = unit / pieces;
-  const int c0 = (int)(unit - n * pieces) * (128 * VEC);
+  constexpr int PER = kFwdPer<VEC>;
+  const int c0 = (int)(unit - n * pieces) * (32 * PER * VEC);
   if (n >= N) return;
   const int64_t id = ids[n];
   const bool ok = id >= 0 && id < V;
   if (!ok && c0 == 0 && lane == 0) report(status, MOE_ERR_DEVICE_CHECK, 501);
   const T* src = table + (ok ? id : 0) * H;
   T* dst = y + n * H;
-  Pack<T, VEC> p[4];
+  Pack<T, VEC> p[PER];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int c = c0 + (i * 32 + lane) * VEC;
     if (c < H) p[i] = load_pack<T, VEC>(src + c);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int c = c0 + (i * 32 + lane) * VEC;
     if (c >= H) continue;
     if (!ok || scale != 1.0f) {
@@ -335,42 +339,12 @@ __device__ __forceinline__ int lower_bound_warp(const uint32_t* keys, int n, uin
 }
 
 // a[k][j] += sum over i < n of dy[order[i]][c + k step + j], in order, eight rows' loads at a time.
-// PACKS (1 or 2) packs a thread sums at a time, `step` columns apart.
+// a[k][j] += sum over i < n of dy[order[i]][c + k step + j] for the PACKS packs below H, in order, eight rows' loads at a
+// time.
 template <int PACKS, class T, int VEC>
 __device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy, const int* order, int n, int c, int step,
                                          int H, float (&a)[PACKS][VEC]) {
-  const bool more = PACKS > 1 && c + step < H;
-  int i = 0;
-  for (; i + 8 <= n; i += 8) {
-    Pack<T, VEC> p[8][PACKS];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const T* row = dy + order[i + r] * lddy + c;
-      p[r][0] = load_pack<T, VEC>(row);
-      if constexpr (PACKS > 1) {
-        p[r][1] = zero_pack<T, VEC>();
-        if (more) p[r][1] = load_pack<T, VEC>(row + step);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-#pragma unroll
-      for (int k = 0; k < PACKS; ++k) {
-        float f[VEC];
-        unpack<T, VEC>(p[r][k], f);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) a[k][j] += f[j];
-      }
-  }
-#pragma unroll 4
-  for (; i < n; ++i) {
-    const T* row = dy + order[i] * lddy + c;
-    Pack<T, VEC> p[PACKS];
-    p[0] = load_pack<T, VEC>(row);
-    if constexpr (PACKS > 1) {
-      p[1] = zero_pack<T, VEC>();
-      if (more) p[1] = load_pack<T, VEC>(row + step);
-    }
+  auto add = [&](const Pack<T, VEC> (&p)[PACKS]) {
 #pragma unroll
     for (int k = 0; k < PACKS; ++k) {
       float f[VEC];
@@ -378,8 +352,35 @@ __device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy,
 #pragma unroll
       for (int j = 0; j < VEC; ++j) a[k][j] += f[j];
     }
+  };
+  auto load = [&](Pack<T, VEC> (&p)[PACKS], int i) {
+    const T* row = dy + order[i] * lddy + c;
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+      p[k] = zero_pack<T, VEC>();
+      if (k == 0 || c + k * step < H) p[k] = load_pack<T, VEC>(row + k * step);
+    }
+  };
+  int i = 0;
+  for (; i + 8 <= n; i += 8) {
+    Pack<T, VEC> p[8][PACKS];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) load(p[r], i + r);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) add(p[r]);
+  }
+#pragma unroll 4
+  for (; i < n; ++i) {
+    Pack<T, VEC> p[PACKS];
+    load(p, i);
+    add(p);
   }
 }
+// Packs a thread sums at a time: single elements need more of them in flight.
+template <int VEC>
+constexpr int kPacks = VEC == 1 ? 4 : 1;
+template <int VEC>
+constexpr int kAddPacks = VEC == 1 ? 4 : 2;
 
 // Piece b covers sorted places [kPiece b, kPiece (b + 1)).  A run longer than kPiece that meets the piece holds
 // its first place or its last: part[b][0] is the sum over the places of the run that holds the first,
@@ -408,15 +409,23 @@ __global__ void __launch_bounds__(256) embed_piece_kernel(const uint32_t* __rest
     if (e - s <= kPiece || (which && s <= p0)) continue;   // short, or the first place's run again
     const int a0 = max(s, p0), a1 = min(e, p1);
     float* out = part + ((int64_t)blockIdx.x * 2 + which) * H;
-    for (int c = (blockIdx.y * 256 + threadIdx.x) * VEC; c < H; c += gridDim.y * 256 * VEC) {
-      float a[1][VEC];
-      Pack<float, VEC> o;
+    constexpr int PACKS = kPacks<VEC>;
+    const int step = 256 * VEC;
+    for (int c = (blockIdx.y * PACKS * 256 + threadIdx.x) * VEC; c < H; c += gridDim.y * PACKS * step) {
+      float a[PACKS][VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a[0][j] = 0.0f;
-      add_rows<1, T, VEC>(dy, lddy, places + (a0 - p0), a1 - a0, c, 0, H, a);
+      for (int k = 0; k < PACKS; ++k)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o.v[j] = a[0][j];
-      store_pack<float, VEC>(out + c, o);
+        for (int j = 0; j < VEC; ++j) a[k][j] = 0.0f;
+      add_rows<PACKS, T, VEC>(dy, lddy, places + (a0 - p0), a1 - a0, c, step, H, a);
+#pragma unroll
+      for (int k = 0; k < PACKS; ++k)
+        if (c + k * step < H) {
+          Pack<float, VEC> o;
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) o.v[j] = a[k][j];
+          store_pack<float, VEC>(out + c + k * step, o);
+        }
     }
   }
 }
@@ -489,16 +498,16 @@ __global__ void __launch_bounds__(256, 4) embed_rows_kernel(const uint32_t* __re
   if (threadIdx.x > 0 && (int)threadIdx.x < rows) first[threadIdx.x] = lower_bound(keys, lo, hi, (uint32_t)(v0 + threadIdx.x));
   __syncthreads();
   for (int r = threadIdx.x / tpr; r < rows; r += 256 / tpr)
-    embed_row<1, false, T, VEC>(order + first[r], dy, lddy, part, dW + (v0 + r) * H, first[r], first[r + 1], H, threadIdx.x & (tpr - 1),
+    embed_row<kPacks<VEC>, false, T, VEC>(order + first[r], dy, lddy, part, dW + (v0 + r) * H, first[r], first[r + 1], H, threadIdx.x & (tpr - 1),
                              tpr, scale);
 }
 
-// Added into a gradient: only rows of tokens that occur.  Block b takes the runs that start at the sorted places
+// Only the rows of tokens that occur: added into a gradient (ADD), or stored over zeros.  Block b takes the runs that start at the sorted places
 // [kHeads b, kHeads (b + 1)), which it sees by itself (searching for its rows as the dense form does cost twice the
 // time: 52 us for 16384 tokens of 2048 columns).
 constexpr int kHeads = 8;
-template <class T, int VEC>
-__global__ void __launch_bounds__(256) embed_add_kernel(const uint32_t* __restrict__ keys,
+template <class T, int VEC, bool ADD>
+__global__ void __launch_bounds__(256) embed_runs_kernel(const uint32_t* __restrict__ keys,
                                                        const int* __restrict__ order, const T* __restrict__ dy,
                                                        int64_t lddy, const float* __restrict__ part,
                                                        float* __restrict__ dW, int N, int V, int H, int tpr,
@@ -533,8 +542,26 @@ __global__ void __launch_bounds__(256) embed_add_kernel(const uint32_t* __restri
   }
   __syncthreads();
   for (int r = threadIdx.x / tpr; r < runs; r += 256 / tpr)
-    embed_row<2, true, T, VEC>(places[r], dy, lddy, part, dW + (int64_t)run_v[r] * H, run_s[r], run_e[r], H,
+    embed_row<kAddPacks<VEC>, ADD, T, VEC>(places[r], dy, lddy, part, dW + (int64_t)run_v[r] * H, run_s[r], run_e[r], H,
                             threadIdx.x & (tpr - 1), tpr, scale);
+}
+
+// out[0 .. n) = 0, from 16-byte boundary to 16-byte boundary with single elements at the ends.  late: it runs beside the
+// kernel before it (the sort, which does not touch `out`, has waited for everything before it and only then lets this
+// one start) and waits for that kernel at its end, so that what follows sees both complete.
+__global__ void __launch_bounds__(256) embed_clear_kernel(float* __restrict__ out, int64_t n, bool late) {
+  if (!late) {
+    pdl_wait();
+    pdl_trigger();
+  }
+  const int64_t head = min(n, (int64_t)((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / 4);
+  const int64_t packs = (n - head) / 4, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  float4* body = reinterpret_cast<float4*>(out + head);
+  for (int64_t i = i0; i < packs; i += (int64_t)gridDim.x * 256) __stcs(body + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+  if (i0 < head) out[i0] = 0.0f;
+  const int64_t tail = head + packs * 4 + i0;
+  if (tail < n && i0 < 4) out[tail] = 0.0f;
+  if (late) pdl_wait();
 }
 
 struct EmbedLayout {
@@ -671,7 +698,8 @@ int moe_embed_forward(const moe_embed_config* cfg, const void* ids, int32_t id_t
         using I = decltype(iv);
         auto go = [&](auto vv) {
           constexpr int VEC = decltype(vv)::value;
-          const int pieces = (c.H + 128 * VEC - 1) / (128 * VEC);
+          constexpr int kRow = 32 * kFwdPer<VEC> * VEC;
+          const int pieces = (c.H + kRow - 1) / kRow;
           const int64_t units = (int64_t)c.N * pieces;
           return launch_pdl(embed_fwd_kernel<T, I, VEC>, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, s,
                             static_cast<const I*>(ids), static_cast<const T*>(table), static_cast<T*>(y), c.N, c.V,
@@ -720,22 +748,37 @@ int moe_embed_backward(const moe_embed_config* cfg, const void* ids, int32_t id_
       auto go = [&](auto vv) {
         constexpr int VEC = decltype(vv)::value;
         const T* g = static_cast<const T*>(dy);
+        // Rows that do not start on 16 bytes are cleared all at once, 16 bytes a store, and those that occur stored after.
+        const bool clear = VEC == 1 && !accumulate;
+        if (clear) {
+          const cudaError_t e = launch_pdl(embed_clear_kernel, dim3(device_sm_count() * 8), dim3(256), 0, s, dW,
+                                           (int64_t)c.V * c.H, launch_chain_mode() >= MOE_CHAIN_LATE);
+          if (e != cudaSuccess) return e;
+        }
         if (c.N > kPiece) {
-          const dim3 grid((c.N + kPiece - 1) / kPiece, std::min(8, (c.H + 256 * VEC - 1) / (256 * VEC)));
+          const dim3 grid((c.N + kPiece - 1) / kPiece, std::min(8, (c.H + 256 * VEC * kPacks<VEC> - 1) / (256 * VEC * kPacks<VEC>)));
           const cudaError_t e = launch_pdl(embed_piece_kernel<T, VEC>, grid, dim3(256), 0, s, keys, order, g, lddy,
                                            part, c.N, c.V, c.H);
           if (e != cudaSuccess) return e;
         }
+        const float* sums = part;
+        int tpr = 1;
+        auto threads = [&](int packs) {   // threads a row: a power of two
+          while (tpr < 256 && tpr * VEC * packs < c.H) tpr *= 2;
+          return tpr;
+        };
+        const dim3 by_run((c.N + kHeads - 1) / kHeads);
+        if (accumulate)
+          return launch_pdl(embed_runs_kernel<T, VEC, true>, by_run, dim3(256), 0, s, keys, order, g, lddy, sums, dW, c.N,
+                            c.V, c.H, threads(kAddPacks<VEC>), c.scale);
+        if (clear)
+          return launch_pdl(embed_runs_kernel<T, VEC, false>, by_run, dim3(256), 0, s, keys, order, g, lddy, sums, dW,
+                            c.N, c.V, c.H, threads(kAddPacks<VEC>), c.scale);
         // rows a block: about 128 KB of gradient, so that the two searches of a block are paid for
         const int R = (int)std::min<int64_t>(256, std::max<int64_t>(1, 32768 / c.H));
         const dim3 grid((unsigned)(((int64_t)c.V + R - 1) / R));
-        int tpr = 1;
-        while (tpr < 256 && tpr * VEC * (accumulate ? 2 : 1) < c.H) tpr *= 2;   // packs a thread: two at a time, or one
-        if (accumulate)
-          return launch_pdl(embed_add_kernel<T, VEC>, dim3((c.N + kHeads - 1) / kHeads), dim3(256), 0, s, keys, order, g,
-                            lddy, static_cast<const float*>(part), dW, c.N, c.V, c.H, tpr, c.scale);
-        return launch_pdl(embed_rows_kernel<T, VEC>, grid, dim3(256), 0, s, keys, order, g, lddy,
-                          static_cast<const float*>(part), dW, c.N, c.V, c.H, R, tpr, c.scale);
+        return launch_pdl(embed_rows_kernel<T, VEC>, grid, dim3(256), 0, s, keys, order, g, lddy, sums, dW, c.N, c.V,
+                          c.H, R, threads(kPacks<VEC>), c.scale);
       };
       if (c.H % 4 == 0 && lddy % 4 == 0 && aligned_to(dy, 4 * ts) && aligned_to(dW, 16))
         return go(std::integral_constant<int, 4>{});

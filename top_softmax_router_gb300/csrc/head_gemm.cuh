@@ -40,11 +40,12 @@ struct HeadGemm {
   float* part_z;
   float* entry_logit;        // [M][K]
   const float* lse;          // [M], natural
-  const float* coef;         // [M]: g T where the row has entries, else 0
+  const float* coef;         // [M]: g T / out_scale where the row has entries, else 0
   const float* q;            // [M][K]
   uint16_t* d;               // [M][ldd]
   int ldd;
   // HEAD_OUT
+  const float* out_scale;    // [1]: what d was divided by
   const float* add;          // [splits][M][ldo] or NULL
   float* out32;              // [splits][M][ldo] or NULL
   uint16_t* out16;           // [M][ldo] or NULL
@@ -176,14 +177,13 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
     }
   } else {
     const int64_t at = ((int64_t)split * p.M + row) * p.ldo + n0;
+    const float scale = *p.out_scale;
 #pragma unroll 1
     for (int c = c0; c < c1; c += 32) {               // N is a multiple of 32 here
       tc_ld32(tacc + c, v);
       if (!ok) continue;
-      if (none) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-      }
+      for (int j = 0; j < 32; ++j) v[j] = none ? 0.0f : v[j] * scale;
       if (p.add) {
         const float4* a = reinterpret_cast<const float4*>(p.add + at + c);
 #pragma unroll
