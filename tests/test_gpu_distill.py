@@ -102,6 +102,34 @@ def test_fp32_weight_gradient(M):
     compare(out, *a, 1.0)
 
 
+def test_outputs_on_16_bytes(M):
+    """Every pointer 16 bytes off a 32-byte boundary, the workspace's too."""
+    from top_softmax_router_gb300 import _lib
+    X, W, ids, t, g = (v.cuda() for v in make(70, 64, 300, 4, seed=12))
+
+    def off(n, dtype):
+        size = torch.empty(0, dtype=dtype).element_size()
+        flat = torch.zeros(n * size + 64, dtype=torch.uint8, device="cuda")
+        return flat[16:16 + n * size].view(dtype)
+
+    X2, W2 = off(X.numel(), X.dtype).view_as(X).copy_(X), off(W.numel(), W.dtype).view_as(W).copy_(W)
+    cfg = M.DistillConfig(N=70, H=64, V=300, K=4, P=2)
+    ref = M.VocabDistill(cfg)
+    loss, lse, _ = ref.forward(X, W, ids, t)
+    for dt in (torch.bfloat16, torch.float32):
+        want = ref.backward(X, W, ids, t, lse, g, dW_dtype=dt)
+        kd = M.VocabDistill(cfg)
+        kd.ws = off(kd.ws.numel() + 256, torch.uint8)
+        got = kd.forward(X2, W2, ids, t)
+        assert torch.equal(got[0], loss) and torch.equal(got[1], lse)
+        dX, dW = off(X.numel(), X.dtype), off(W.numel(), dt)
+        _lib.check(_lib.load().moe_distill_backward(
+            kd._c(70), X2.data_ptr(), W2.data_ptr(), ids.data_ptr(), t.data_ptr(), lse.data_ptr(), g.data_ptr(),
+            dX.data_ptr(), dW.data_ptr(), 1 if dt == torch.bfloat16 else 0, kd.ws.data_ptr(), kd.ws.numel(),
+            torch.cuda.current_stream().cuda_stream), "moe_distill_backward")
+        assert torch.equal(dX.view_as(want[0]), want[0]) and torch.equal(dW.view_as(want[1]), want[1])
+
+
 def test_rows_with_fewer_entries_or_none(M):
     X, W, ids, t, g = make(140, 128, 700, 12, seed=3)
     ids[0] = -1

@@ -138,48 +138,63 @@ __device__ __forceinline__ void fold2(float& m, float& z, float m2, float z2) {
   m = mn;
 }
 
-// 32 rows a block: lse from the half tiles' pairs (warp w takes half tiles w, w + 8, .. in order, then the warps are
-// folded in order), and the loss from the entries' logits.
-__global__ void __launch_bounds__(256) distill_loss_kernel(const float* __restrict__ part_m,
-                                                           const float* __restrict__ part_z,
-                                                           const float* __restrict__ entry_logit,
-                                                           const float* __restrict__ q,
-                                                           const int32_t* __restrict__ cls,
-                                                           const float* __restrict__ qlogq, float* __restrict__ loss,
-                                                           float* __restrict__ lse, int N, int K, int parts, float T) {
+// 32 rows a block: lse from the half tiles' pairs (warp w takes half tiles w, w + 32, .. in order, four loads at a time;
+// then the warps are folded in order), and the loss from the entries' logits, a row a warp.
+__global__ void __launch_bounds__(1024) distill_loss_kernel(const float* __restrict__ part_m,
+                                                            const float* __restrict__ part_z,
+                                                            const float* __restrict__ entry_logit,
+                                                            const float* __restrict__ q,
+                                                            const int32_t* __restrict__ cls,
+                                                            const float* __restrict__ qlogq, float* __restrict__ loss,
+                                                            float* __restrict__ lse, int N, int K, int parts, float T) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sm[8][32], sz[8][32], s_lse[32];
+  __shared__ float sm[32][33], sz[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * 32, row = r0 + lane;
-  float m = -INFINITY, z = 0.0f;
-  if (row < N)
-    for (int i = warp; i < parts; i += 8) fold2(m, z, part_m[(int64_t)i * N + row], part_z[(int64_t)i * N + row]);
-  sm[warp][lane] = m;
-  sz[warp][lane] = z;
-  __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < 8; ++w) fold2(m, z, sm[w][lane], sz[w][lane]);
-    const float l = m * 0.6931471805599453f + logf(z);
-    s_lse[lane] = l;
-    if (row < N) lse[row] = l;
+  const int r0 = blockIdx.x * 32;
+  {
+    const int row = r0 + lane;
+    float m = -INFINITY, z = 0.0f;
+    if (row < N)
+      for (int i = warp; i < parts; i += 128) {
+        float pm[4], pz[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = i + 32 * k < parts;
+          pm[k] = in ? part_m[(int64_t)(i + 32 * k) * N + row] : -INFINITY;
+          pz[k] = in ? part_z[(int64_t)(i + 32 * k) * N + row] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) fold2(m, z, pm[k], pz[k]);
+      }
+    sm[lane][warp] = m;
+    sz[lane][warp] = z;
   }
   __syncthreads();
+  // warp w: row r0 + w; the fold of its 32 pairs is a fixed tree
+  const int row = r0 + warp;
+  if (row >= N) return;
+  float m = sm[warp][lane], z = sz[warp][lane];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, off), z2 = __shfl_xor_sync(0xffffffffu, z, off);
+    fold2(m, z, m2, z2);
+  }
+  const float l = m * 0.6931471805599453f + logf(z);
   const float inv_t = 1.0f / T;
-  for (int k = 0; k < 4; ++k) {
-    const int i = warp * 4 + k;
-    if (r0 + i >= N) break;
-    const int64_t base = (int64_t)(r0 + i) * K;
-    float a = 0.0f;
-    bool some = false;
-    for (int j = lane; j < K; j += 32)
-      if (cls[base + j] >= 0) {
-        a = fmaf(q[base + j], s_lse[i] - entry_logit[base + j] * inv_t, a);
-        some = true;
-      }
-    a = warp_sum(a);
-    some = __any_sync(0xffffffffu, some);
-    if (lane == 0) loss[r0 + i] = some ? T * T * (qlogq[r0 + i] + a) : 0.0f;
+  const int64_t base = (int64_t)row * K;
+  float a = 0.0f;
+  bool some = false;
+  for (int j = lane; j < K; j += 32)
+    if (cls[base + j] >= 0) {
+      a = fmaf(q[base + j], l - entry_logit[base + j] * inv_t, a);
+      some = true;
+    }
+  a = warp_sum(a);
+  some = __any_sync(0xffffffffu, some);
+  if (lane == 0) {
+    lse[row] = l;
+    loss[row] = some ? T * T * (qlogq[row] + a) : 0.0f;
   }
 }
 
@@ -359,7 +374,7 @@ int moe_distill_forward(const moe_distill_config* cfg, const uint16_t* X, const 
          })) != MOE_OK)
       return v;
     if ((v = timed_launch(MOE_K_DISTILL_LOSS, "distill loss", s, [&] {
-           return launch_pdl(distill_loss_kernel, dim3(L.groups), dim3(256), 0, s, static_cast<const float*>(p.part_m),
+           return launch_pdl(distill_loss_kernel, dim3(L.groups), dim3(1024), 0, s, static_cast<const float*>(p.part_m),
                              static_cast<const float*>(p.part_z), static_cast<const float*>(p.entry_logit), p.q,
                              reinterpret_cast<const int32_t*>(w + L.cls),
                              reinterpret_cast<const float*>(w + L.qlogq), loss, lse, c.N, c.K, 2 * L.tiles,

@@ -50,6 +50,7 @@ struct HeadGemm {
   float* out32;              // [splits][M][ldo] or NULL
   uint16_t* out16;           // [M][ldo] or NULL
   int ldo;
+  bool sectors;              // d and the outputs (whose rows are multiples of 64 bytes) lie on 32 bytes
 };
 
 // The tensor cores cut each addition to an accumulator off towards zero, so that a logit of H products comes out too
@@ -114,6 +115,43 @@ __device__ __forceinline__ void tc_st32(uint32_t taddr, const float* v) {
       : "memory");
 }
 
+// 32 bytes to a 32-byte boundary in one store: a whole sector (two of 16 reach L2 as two partial writes of it, and
+// dW of 53 tokens x 640 x 60341 classes went out at 2 TB/s).
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// 32 values, rounded to bf16 or as they are.  sectors: dst lies on 32 bytes.
+__device__ __forceinline__ void store_row16(uint16_t* dst, const float (&v)[32], bool sectors) {
+  if (!sectors) {
+    store_bf16x32(dst, v);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[16 * h + 2 * j], v[16 * h + 2 * j + 1]);
+    store_sector(dst + 16 * h, w);
+  }
+}
+__device__ __forceinline__ void store_row32(float* dst, const float (&v)[32], bool sectors) {
+  if (!sectors) {
+    float4* o = reinterpret_cast<float4*>(dst);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * h + j]);
+    store_sector(dst + 8 * h, w);
+  }
+}
+
 // The epilogue of one warp: rows row0 + lane (valid below p.M), the columns c0 .. c0 + 127 of column tile nt.  none: the
 // tile's share of K is empty, and its accumulator holds nothing.
 template <int EPI>
@@ -156,7 +194,7 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
       tc_ld32(tacc + c, v);
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = coef == 0.0f ? 0.0f : coef * exp2_fast(fmaf(v[j], p.to_log2, -l));
-      if (ok) store_bf16x32(d + c, v);
+      if (ok) store_row16(d + c, v, p.sectors);
     }
     if (row0 < p.M) {
       const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
@@ -192,12 +230,8 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
           v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
         }
       }
-      if (p.out32) {
-        float4* o = reinterpret_cast<float4*>(p.out32 + at + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      }
-      if (p.out16) store_bf16x32(p.out16 + at + c, v);
+      if (p.out32) store_row32(p.out32 + at + c, v, p.sectors);
+      if (p.out16) store_row16(p.out16 + at + c, v, p.sectors);
     }
   }
   if constexpr (EPI == HEAD_LSE) {
@@ -443,6 +477,8 @@ cudaError_t launch_head_gemm(const CUtensorMap& a, const CUtensorMap& b, HeadGem
   p.tiles_m = (p.M + 255) / 256;
   p.tiles_n = (p.N + 255) / 256;
   if (p.splits < 1) p.splits = 1;
+  p.sectors = ((reinterpret_cast<uintptr_t>(p.out16) | reinterpret_cast<uintptr_t>(p.out32) |
+               reinterpret_cast<uintptr_t>(p.d)) & 31) == 0;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, HeadSmem::TOTAL);
