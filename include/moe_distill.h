@@ -18,7 +18,8 @@
  *
  * Schedule: that of moe_ce.h.  Forward: one tcgen05 GEMM whose epilogue folds each logit tile in tensor
  * memory into (max, sum) pairs and picks out the entries' logits.  Backward: for each of P vocabulary
- * strips the logits are recomputed, d is written for that strip only, dX accumulates d W_strip in fp32
+ * strips (one where d of the whole vocabulary takes at most 8 MB) the logits are recomputed, d is written for that
+ * strip only, dX accumulates d W_strip in fp32
  * and dW_strip = d^T X is written.
  *
  * Conventions are those of moe.h (MOE_OK / MOE_ERR_* codes, stream as void*, asynchronous, capturable,

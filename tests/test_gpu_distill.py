@@ -86,6 +86,20 @@ def test_against_the_oracle(M, N, H, V, K, P, T):
     compare(run(M, *a, P=P, T=T), *a, T)
 
 
+@pytest.mark.parametrize("N,H,V,K,P,T", [(511, 64, 9001, 8, 8, 1.0), (1030, 128, 4500, 33, 3, 2.0), (2100, 64, 2049, 5, 2, 1.0),
+                                         (300, 320, 20000, 16, 4, 4.0)])
+def test_several_strips(M, N, H, V, K, P, T):
+    """d of more than 8 MB: P strips, the last one narrower; the strip count changes dX's rounding alone."""
+    a = make(N, H, V, K, seed=P)
+    out, one = run(M, *a, P=P, T=T), run(M, *a, P=1, T=T)
+    compare(out, *a, T)
+    assert all(torch.equal(out[i], one[i]) for i in (0, 1, 2, 4))
+    unit = M.VocabDistill(M.DistillConfig(N=N, H=H, V=V, K=K, P=P, temperature=T))
+    b = make(7, H, V, K, seed=P + 1)          # fewer tokens in the same workspace: one strip
+    compare(run(M, *b, T=T, unit=unit), *b, T)
+    assert all(torch.equal(p, q) for p, q in zip(out, run(M, *a, T=T, unit=unit)))
+
+
 @pytest.mark.parametrize("N,H,V,P", [(40, 64, 6000, 1), (300, 128, 9000, 2), (256, 320, 5121, 1), (1, 64, 20000, 3)])
 def test_shares_of_a_long_strip(M, N, H, V, P):
     """Few tiles of dX and many classes: K is split, the last share and strip are short or empty."""

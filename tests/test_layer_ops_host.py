@@ -112,7 +112,7 @@ def test_distill_shapes(lib, cfg, code):
     assert lib.load().moe_distill_workspace_bytes(ref(lib.DistillConfig(*cfg)), None, None) == code
 
 
-@pytest.mark.parametrize("H,V,P", [(64, 70000, 1), (1024, 32000, 4), (4096, 65536, 4), (320, 5000, 2), (64, 100, 3)])
+@pytest.mark.parametrize("H,V,P", [(64, 70000, 1), (64, 70000, 9), (1024, 32000, 4), (4096, 65536, 4), (320, 5000, 2), (64, 100, 3)])
 def test_a_distill_workspace_serves_fewer_tokens(lib, H, V, P):
     f, b, last = ctypes.c_size_t(), ctypes.c_size_t(), (0, 0)
     for n in list(range(0, 600, 7)) + [1023, 1024, 1025, 2048, 5000, 8192, 30000]:

@@ -21,6 +21,9 @@ constexpr int kGroup = 32;        // rows of a bucket
 // Row tiles of a band: the ~76 clusters at work then hold 8 x ~10 tiles, 36 MB of operands at H = 4096.
 constexpr int kHeadBand = 8;
 constexpr int kClusters = 76;     // CTA pairs of the GPU
+// A d of the whole vocabulary of at most this is one strip whatever P: three launches instead of 3 P (53 x 640 x 60341,
+// P = 3: 168 us of backward instead of 220).
+constexpr int64_t kOneStrip = 8 << 20;
 
 // One block a group of 32 rows, a row a warp: q of each entry, equal classes of a row joined at the first of
 // them (class[j] = -1 for every other), the row's sum of q log q, and the group's entries by class tile.
@@ -246,7 +249,8 @@ DistillLayout distill_layout(const moe_distill_config& c) {
   const int64_t N = c.N, V = c.V, K = c.K;
   L.groups = (int)((N + kGroup - 1) / kGroup);
   L.tiles = (int)((V + 255) / 256);
-  L.Vs = (int)(((V + c.P - 1) / c.P + 255) / 256 * 256);
+  const int64_t whole = (int64_t)L.tiles * 256, strip = ((V + c.P - 1) / c.P + 255) / 256 * 256;
+  L.Vs = (int)(N * whole * 2 <= kOneStrip ? whole : strip);
   L.S = (int)((V + L.Vs - 1) / L.Vs);
   // dX has N x H tiles of 256 x 256 and a long K: where its tiles fill less than half of the 76 clusters, each strip's
   // K is split among them, at least 8 blocks of 64 classes to a share.  (2048 x 1024 from 8192 classes a strip, 32
@@ -272,9 +276,10 @@ DistillLayout distill_layout(const moe_distill_config& c) {
   L.entry_logit = take((size_t)N * K * 4);
   L.fwd_total = o;
   o = common;
-  L.d = take((size_t)N * L.Vs * 2);
+  // (a workspace serves fewer tokens too, whose one strip may be larger)
+  L.d = take((size_t)std::max(N * L.Vs * 2, std::min(N, kOneStrip / (whole * 2)) * whole * 2));
   // rows of fp32: N, or shares x N of any smaller N (a workspace serves fewer tokens too)
-  const int64_t most = std::min<int64_t>(L.Vs / 512, kClusters / tiles_n);   // shares of a single row tile
+  const int64_t most = std::min<int64_t>(whole / 512, kClusters / tiles_n);   // shares of a single row tile
   const int64_t rows = std::max<int64_t>(L.S > 1 ? N : 0, most > 1 ? std::min<int64_t>(N * most, 256 * kClusters / tiles_n) : 0);
   L.acc = take((size_t)rows * c.H * 4);
   L.bwd_total = o;
