@@ -82,12 +82,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// One fp32 column of tensor memory: each thread gets its lane's value.
-__device__ __forceinline__ float tc_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  return __uint_as_float(r);
+// Four single fp32 columns of tensor memory: each thread gets its lane's values.  (The wait names the registers, so that
+// nothing can use them before it.)
+__device__ __forceinline__ void tc_ld_columns(const uint32_t (&taddr)[4], float (&v)[4]) {
+  uint32_t r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[k]) : "r"(taddr[k]));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(r[k]);
 }
 
 // v[j] += this thread's lane of 16 consecutive fp32 columns of tensor memory.
@@ -98,7 +102,11 @@ __device__ __forceinline__ void tc_add16(uint32_t taddr, float* v) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
 }
@@ -156,11 +164,70 @@ __device__ __forceinline__ void store_row32(float* dst, const float (&v)[32], bo
   }
 }
 
+// What a tile's epilogue reads besides its accumulator, loaded while the main loop still runs.
+struct HeadRow {
+  float coef, l, q;   // HEAD_D: the row's coefficient and lse in powers of two; q of the lane's record
+  int e0, e1;         // the entries of these 32 rows and this class tile
+  uint32_t rec;       // the lane's among the first 32
+};
+template <int EPI>
+__device__ __forceinline__ void load_records(const HeadGemm& p, int row0, int e0, int e1, int lane, uint32_t& rec, float& q) {
+  rec = 0;
+  q = 0.0f;
+  if (e0 + lane < e1) {
+    rec = p.entry[e0 + lane];
+    if (EPI == HEAD_D) q = p.q[(int64_t)(row0 + (int)(rec & 31)) * p.K + (rec >> 13)];
+  }
+}
+template <int EPI>
+__device__ __forceinline__ HeadRow head_row(const HeadGemm& p, int row0, int nt, int lane) {
+  HeadRow r = {0.0f, 0.0f, 0.0f, 0, 0, 0};
+  if (EPI == HEAD_OUT || row0 >= p.M) return r;
+  const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
+  r.e0 = b[0];
+  r.e1 = b[1];
+  if (EPI == HEAD_D && row0 + lane < p.M) {
+    r.coef = p.coef[row0 + lane];
+    r.l = p.lse[row0 + lane] * 1.4426950408889634f;
+  }
+  load_records<EPI>(p, row0, r.e0, r.e1, lane, r.rec, r.q);
+  return r;
+}
+// f(record, q, logit) for each entry in this warp's half of the columns, four of them a load of tensor memory; the whole
+// warp calls it for every record, with its own lane's logit.
+template <int EPI, class F>
+__device__ __forceinline__ void for_entries(const HeadGemm& p, const HeadRow& pre, int row0, int half, uint32_t tacc,
+                                            int lane, F&& f) {
+  uint32_t recs = pre.rec;
+  float qs = pre.q;
+  for (int e0 = pre.e0; e0 < pre.e1; e0 += 32) {
+    if (e0 != pre.e0) load_records<EPI>(p, row0, e0, pre.e1, lane, recs, qs);
+    uint32_t left = __ballot_sync(0xffffffffu, e0 + lane < pre.e1 && (int)((recs >> 12) & 1) == half);
+    while (left) {
+      uint32_t rec[4], at[4];
+      float q[4], y[4];
+      const int n = min(4, __popc(left));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int src = left ? __ffs(left) - 1 : 0;
+        left &= left - 1;
+        rec[k] = __shfl_sync(0xffffffffu, recs, src);
+        q[k] = __shfl_sync(0xffffffffu, qs, src);
+        at[k] = tacc + ((rec[k] >> 5) & 255);
+      }
+      tc_ld_columns(at, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < n) f(rec[k], q[k], y[k]);
+    }
+  }
+}
+
 // The epilogue of one warp: rows row0 + lane (valid below p.M), the columns c0 .. c0 + 127 of column tile nt.  none: the
 // tile's share of K is empty, and its accumulator holds nothing.
 template <int EPI>
-__device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int nt, int half, int split, bool none,
-                                              uint32_t tacc, int lane) {
+__device__ __forceinline__ void head_epilogue(const HeadGemm& p, const HeadRow& pre, int row0, int nt, int half, int split,
+                                              bool none, uint32_t tacc, int lane) {
   const int row = row0 + lane;
   const bool ok = row < p.M;
   const int n0 = nt * 256;
@@ -190,8 +257,7 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
       p.part_z[(int64_t)(2 * nt + half) * p.M + row] = z;
     }
   } else if constexpr (EPI == HEAD_D) {
-    const float coef = ok ? p.coef[row] : 0.0f;
-    const float l = ok ? p.lse[row] * 1.4426950408889634f : 0.0f;
+    const float coef = pre.coef, l = pre.l;
     uint16_t* d = p.d + (int64_t)row * p.ldd + n0;
 #pragma unroll 1
     for (int c = c0; c < c1; c += 32) {
@@ -200,23 +266,10 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
       for (int j = 0; j < 32; ++j) v[j] = coef == 0.0f ? 0.0f : coef * exp2_fast(fmaf(v[j], p.to_log2, -l));
       if (ok) store_row16(d + c, v, p.sectors);
     }
-    if (row0 < p.M) {
-      const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
-      const int e1 = b[1];
-      for (int e0 = b[0]; e0 < e1; e0 += 32) {        // 32 records (and their q) a load
-        const uint32_t recs = e0 + lane < e1 ? p.entry[e0 + lane] : 0;
-        const float qs = e0 + lane < e1 ? p.q[(int64_t)(row0 + (int)(recs & 31)) * p.K + (recs >> 13)] : 0.0f;
-        const int n = min(32, e1 - e0);
-        for (int i = 0; i < n; ++i) {
-          const uint32_t rec = __shfl_sync(0xffffffffu, recs, i);
-          const int c = (rec >> 5) & 255;
-          if ((c >> 7) != half) continue;             // the same for the whole warp
-          const float q = __shfl_sync(0xffffffffu, qs, i), y = tc_ld1(tacc + c);
-          if (ok && lane == (int)(rec & 31))           // this thread wrote the element above
-            d[c] = __bfloat16_as_ushort(__float2bfloat16_rn(coef * (exp2_fast(fmaf(y, p.to_log2, -l)) - q)));
-        }
-      }
-    }
+    for_entries<EPI>(p, pre, row0, half, tacc, lane, [&](uint32_t rec, float q, float y) {
+      if (ok && lane == (int)(rec & 31))                // this thread wrote the element above
+        d[(rec >> 5) & 255] = __bfloat16_as_ushort(__float2bfloat16_rn(coef * (exp2_fast(fmaf(y, p.to_log2, -l)) - q)));
+    });
   } else {
     const int64_t at = ((int64_t)split * p.M + row) * p.ldo + n0;
     const float scale = *p.out_scale;
@@ -238,23 +291,10 @@ __device__ __forceinline__ void head_epilogue(const HeadGemm& p, int row0, int n
       if (p.out16) store_row16(p.out16 + at + c, v, p.sectors);
     }
   }
-  if constexpr (EPI == HEAD_LSE) {
-    if (row0 < p.M) {
-      const int* b = p.bucket + (int64_t)(row0 >> 5) * (p.tiles_all + 1) + p.tile0 + nt;
-      const int e1 = b[1];
-      for (int e0 = b[0]; e0 < e1; e0 += 32) {
-        const uint32_t recs = e0 + lane < e1 ? p.entry[e0 + lane] : 0;
-        const int n = min(32, e1 - e0);
-        for (int i = 0; i < n; ++i) {
-          const uint32_t rec = __shfl_sync(0xffffffffu, recs, i);
-          const int c = (rec >> 5) & 255;
-          if ((c >> 7) != half) continue;
-          const float y = tc_ld1(tacc + c);
-          if (ok && lane == (int)(rec & 31)) p.entry_logit[(int64_t)row * p.K + (rec >> 13)] = y;
-        }
-      }
-    }
-  }
+  if constexpr (EPI == HEAD_LSE)
+    for_entries<EPI>(p, pre, row0, half, tacc, lane, [&](uint32_t rec, float, float y) {
+      if (ok && lane == (int)(rec & 31)) p.entry_logit[(int64_t)row * p.K + (rec >> 13)] = y;
+    });
 }
 
 // Tile w: bands of p.band row tiles; within a band the row tile varies fastest, so that the clusters at work share a
@@ -430,6 +470,8 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
     for (int w = cluster; w < total && ok; w += clusters) {
       int mt, nt, kb0, kb1, split;
       head_tile(p, w, &mt, &nt, &kb0, &kb1, &split);
+      const int row0 = mt * 256 + 128 * (int)rank + q * 32;
+      const HeadRow pre = head_row<EPI>(p, row0, nt, lane);
       const int accs = EPI == HEAD_LSE ? (p.nk + p.share - 1) / p.share : 1;
       float sum[EPI == HEAD_LSE ? 128 : 1];   // of the accumulators so far
       if constexpr (EPI == HEAD_LSE) {
@@ -458,7 +500,7 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
           }
         }
         if (a + 1 == accs)
-          head_epilogue<EPI>(p, mt * 256 + 128 * (int)rank + q * 32, nt, half, split, kb0 == kb1, tacc, lane);
+          head_epilogue<EPI>(p, pre, row0, nt, half, split, kb0 == kb1, tacc, lane);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
