@@ -774,14 +774,16 @@ int moe_embed_backward(const moe_embed_config* cfg, const void* ids, int32_t id_
         if (accumulate)
           return launch_pdl(embed_runs_kernel<T, VEC, true>, by_run, dim3(256), 0, s, keys, order, g, lddy, sums, dW, c.N,
                             c.V, c.H, threads(kAddPacks<VEC>), c.scale);
-        if (clear)
+        if constexpr (VEC == 1) {
           return launch_pdl(embed_runs_kernel<T, VEC, false>, by_run, dim3(256), 0, s, keys, order, g, lddy, sums, dW,
                             c.N, c.V, c.H, threads(kAddPacks<VEC>), c.scale);
-        // rows a block: about 128 KB of gradient, so that the two searches of a block are paid for
-        const int R = (int)std::min<int64_t>(256, std::max<int64_t>(1, 32768 / c.H));
-        const dim3 grid((unsigned)(((int64_t)c.V + R - 1) / R));
-        return launch_pdl(embed_rows_kernel<T, VEC>, grid, dim3(256), 0, s, keys, order, g, lddy, sums, dW, c.N, c.V,
-                          c.H, R, threads(kPacks<VEC>), c.scale);
+        } else {
+          // rows a block: about 128 KB of gradient, so that the two searches of a block are paid for
+          const int R = (int)std::min<int64_t>(256, std::max<int64_t>(1, 32768 / c.H));
+          const dim3 grid((unsigned)(((int64_t)c.V + R - 1) / R));
+          return launch_pdl(embed_rows_kernel<T, VEC>, grid, dim3(256), 0, s, keys, order, g, lddy, sums, dW, c.N, c.V,
+                            c.H, R, threads(kPacks<VEC>), c.scale);
+        }
       };
       if (c.H % 4 == 0 && lddy % 4 == 0 && aligned_to(dy, 4 * ts) && aligned_to(dW, 16))
         return go(std::integral_constant<int, 4>{});

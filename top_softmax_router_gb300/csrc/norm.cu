@@ -2,7 +2,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "../../include/moe.h"
@@ -12,19 +11,20 @@
 namespace moe {
 namespace {
 
-// A row is held in registers by `tpr` threads (a multiple of 32), PER packs of VEC elements each: pack i of
-// thread t holds columns VEC (t + i tpr) ..  A block holds block / tpr rows at a time.
-// Sums of two values over the tpr threads of a row: one shuffle tree per warp, then the warps' sums in
-// order.  `red`: 2 x 32 floats of shared memory, used alternately by the caller (`slot`).
+// A row is held in registers by TPR threads (a multiple of 32), PER packs of VEC elements each: pack i of
+// thread t holds columns VEC (t + i TPR) ..  A block of THREADS holds THREADS / TPR rows at a time: four rows of a
+// warp each, or one.
+//
+// Sums of two values over the tpr threads of a row: a shuffle tree in each warp, then one over the warps' sums.
+// `red`: the caller uses two of them in turn.
 __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* red) {
   a = warp_sum(a);
   b = warp_sum(b);
   if (tpr == 32) return make_float2(a, b);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = tpr >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) red[warp] = make_float2(a, b);
   __syncthreads();
-  const int w0 = warp / warps * warps;
-  const float2 v = lane < warps ? red[w0 + lane] : make_float2(0.0f, 0.0f);
+  const float2 v = lane < tpr >> 5 ? red[lane] : make_float2(0.0f, 0.0f);   // one row a block
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
@@ -476,8 +476,11 @@ cudaError_t fwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx,
   if (packs <= 512) return fwd_launch<T, P, VEC, 4, 128, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
   if (packs <= 1024) return fwd_launch<T, P, VEC, 8, 128, 8>(c, x, ldx, weight, bias, y, mean, rstd, s);
   if (packs <= 2048) return fwd_launch<T, P, VEC, 8, 256, 4>(c, x, ldx, weight, bias, y, mean, rstd, s);
-  if (packs <= 4096) return fwd_launch<T, P, VEC, 16, 256, 2>(c, x, ldx, weight, bias, y, mean, rstd, s);
-  return fwd_launch<T, P, VEC, 16, 1024, 1>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  if constexpr (MOE_LAYERNORM_MAX_H / VEC > 2048) {
+    if (packs <= 4096) return fwd_launch<T, P, VEC, 16, 256, 2>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  }
+  if constexpr (VEC == 1) return fwd_launch<T, P, VEC, 16, 1024, 1>(c, x, ldx, weight, bias, y, mean, rstd, s);
+  return cudaErrorInvalidValue;   // no row is wider
 }
 
 template <class T, class P, int VEC, int PER, int TPR, int BLOCKS>
@@ -522,8 +525,9 @@ cudaError_t bwd_ring_launch(const moe_layernorm_config& c, const RingShape& r, c
                     wait_limit_ns());
 }
 
-// A warp holds rows of up to 128 packs.  Wider rows of 16-byte packs go through the ring of shared memory where a block
-// has threads for them and three places (H up to 13312 in 16 bits, 7680 in fp32); the others stay in a block's
+// A warp holds rows of up to 128 packs (one pack a thread, or four: the register form of 32768 x 7168 took 462 us, the
+// ring 230, but the ring's threads would stand idle below).  Wider rows of 16-byte packs go through the ring of shared memory where a block
+// has threads for them and three places (H up to 14336 in 16 bits, 7680 in fp32); the others stay in a block's
 // registers.
 template <class T, class P, int VEC>
 cudaError_t bwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight, const float* mean,
