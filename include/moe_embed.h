@@ -4,7 +4,7 @@
  *
  *   y[n]  = scale table[ids[n]]                          (fp32 product, rounded to the table's type)
  *   dW[v] = scale sum over the n with ids[n] = v of dy[n]   (fp32, summed in ascending n in pieces
- *           of 64 tokens, so the same inputs always give the same bits)
+ *           of 32 tokens, so the same inputs always give the same bits)
  *
  * Conventions are those of moe.h (MOE_OK / MOE_ERR_* codes, stream as void*, asynchronous, capturable,
  * the caller owns every buffer and the workspace), and:

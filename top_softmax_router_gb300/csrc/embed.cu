@@ -16,7 +16,7 @@
 namespace moe {
 namespace {
 
-constexpr int kPiece = 64;           // positions of a piece of a long run
+constexpr int kPiece = 32;           // positions of a piece of a long run (64: 16384 x 2048 added 162 us a pass, 32: 157, 16: 170)
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kTile = 8192;          // most positions sorted by one block
