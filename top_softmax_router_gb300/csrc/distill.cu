@@ -151,10 +151,11 @@ __global__ void __launch_bounds__(1024) distill_loss_kernel(const float* __restr
                                                             const float* __restrict__ q,
                                                             const int32_t* __restrict__ cls,
                                                             const float* __restrict__ qlogq, float* __restrict__ loss,
-                                                            float* __restrict__ lse, int N, int K, int parts, float T) {
+                                                            float* __restrict__ lse, float* __restrict__ mean, int N,
+                                                            int K, int parts, float T) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sm[32][33], sz[32][33];
+  __shared__ float sm[32][33], sz[32][33], s_loss[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = blockIdx.x * 32;
   {
@@ -178,28 +179,39 @@ __global__ void __launch_bounds__(1024) distill_loss_kernel(const float* __restr
   __syncthreads();
   // warp w: row r0 + w; the fold of its 32 pairs is a fixed tree
   const int row = r0 + warp;
-  if (row >= N) return;
-  float m = sm[warp][lane], z = sz[warp][lane];
+  float value = 0.0f;
+  if (row < N) {
+    float m = sm[warp][lane], z = sz[warp][lane];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, off), z2 = __shfl_xor_sync(0xffffffffu, z, off);
-    fold2(m, z, m2, z2);
-  }
-  const float l = m * 0.6931471805599453f + logf(z);
-  const float inv_t = 1.0f / T;
-  const int64_t base = (int64_t)row * K;
-  float a = 0.0f;
-  bool some = false;
-  for (int j = lane; j < K; j += 32)
-    if (cls[base + j] >= 0) {
-      a = fmaf(q[base + j], l - entry_logit[base + j] * inv_t, a);
-      some = true;
+    for (int off = 16; off > 0; off >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, off), z2 = __shfl_xor_sync(0xffffffffu, z, off);
+      fold2(m, z, m2, z2);
     }
-  a = warp_sum(a);
-  some = __any_sync(0xffffffffu, some);
-  if (lane == 0) {
-    lse[row] = l;
-    loss[row] = some ? T * T * (qlogq[row] + a) : 0.0f;
+    const float l = m * 0.6931471805599453f + logf(z);
+    const float inv_t = 1.0f / T;
+    const int64_t base = (int64_t)row * K;
+    float a = 0.0f;
+    bool some = false;
+    for (int j = lane; j < K; j += 32)
+      if (cls[base + j] >= 0) {
+        a = fmaf(q[base + j], l - entry_logit[base + j] * inv_t, a);
+        some = true;
+      }
+    a = warp_sum(a);
+    some = __any_sync(0xffffffffu, some);
+    value = some ? T * T * (qlogq[row] + a) : 0.0f;
+    if (lane == 0) {
+      lse[row] = l;
+      loss[row] = value;
+    }
+  }
+  if (!mean) return;
+  // the only block also takes the mean, as distill_mean_kernel would
+  if (lane == 0) s_loss[warp] = value;
+  __syncthreads();
+  if (warp == 0) {
+    value = warp_sum(s_loss[lane]);
+    if (lane == 0) *mean = value / (float)N;
   }
 }
 
@@ -384,12 +396,13 @@ int moe_distill_forward(const moe_distill_config* cfg, const uint16_t* X, const 
            return launch_pdl(distill_loss_kernel, dim3(L.groups), dim3(1024), 0, s, static_cast<const float*>(p.part_m),
                              static_cast<const float*>(p.part_z), static_cast<const float*>(p.entry_logit), p.q,
                              reinterpret_cast<const int32_t*>(w + L.cls),
-                             reinterpret_cast<const float*>(w + L.qlogq), loss, lse, c.N, c.K, 2 * L.tiles,
+                             reinterpret_cast<const float*>(w + L.qlogq), loss, lse,
+                             L.groups == 1 ? loss_mean : static_cast<float*>(nullptr), c.N, c.K, 2 * L.tiles,
                              c.temperature);
          })) != MOE_OK)
       return v;
   }
-  if (!loss_mean) return MOE_OK;
+  if (!loss_mean || L.groups == 1) return MOE_OK;
   return timed_launch(MOE_K_DISTILL_LOSS, "distill mean", s, [&] {
     return launch_pdl(distill_mean_kernel, dim3(1), dim3(1024), 0, s, static_cast<const float*>(loss), loss_mean, c.N);
   });
