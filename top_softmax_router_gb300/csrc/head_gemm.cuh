@@ -9,9 +9,9 @@
 // Warps of a CTA (320 threads): 0 loads, 1 issues the MMAs (even CTA), 2..9 are the epilogue: two for each quarter of
 // the tensor memory's lanes, one for each half of the tile's columns.
 //
-// Bound by the tensor cores at size (8192 x 4096 x 65536, 4.4 TFLOP each: logits 2.69 ms, 1.64 PFLOP/s; d 2.72; dX 2.80;
-// dW 2.83, under the power cap), by whole waves of tiles on 76 clusters below (2048 x 1024 x 32000: logits 102 us, 1.31
-// PFLOP/s), and by launch and load latency where there are few tiles (300 x 128 x 1000: 11 to 17 us each).
+// Bound by the tensor cores at size (8192 x 4096 x 65536, 4.4 TFLOP each: logits 2.85 ms, 1.54 PFLOP/s; d 2.72; dX 2.80;
+// dW 2.83, under the power cap), by whole waves of tiles on 76 clusters below (2048 x 1024 x 32000: logits 104 us, 1.29
+// PFLOP/s), and by launch and load latency where there are few tiles (300 x 128 x 1000: 10 to 14 us each).
 //
 // Every wait is bounded (wait_bounded): a wait that runs out sets the workspace status, and both CTAs leave.
 #pragma once

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 // Persistent: block b takes row groups b, b + grid, ..  x and dy are read once; dx is written, and each
 // thread keeps the sums of dy xh and dy of its columns in registers over all its rows.  The block's sums
 // go to part[block][2][H]; norm_param_kernel adds the blocks in order, so the result has a fixed order.
-// Places past the row (and rows past the last) hold dy = 0, which adds nothing.  4099 x 1001 fp32: 16 us, 3.1 TB/s.
+// Places past the row (and rows past the last) hold dy = 0, which adds nothing.  4099 x 1001 fp32: 15 us, 3.3 TB/s.
 template <class T, class P, int VEC, int PER, int TPR, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
     norm_bwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__ weight, const float* __restrict__ mean,
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 // sums.  The copies run ahead of the reductions, so the memory stays busy, and the blocks that share an SM work while
 // the others meet.  The weight lies in shared memory in fp32.  A thread whose last packs are past the row reads
 // the row's last pack in their place and adds nothing, so that the arithmetic has no branches.  Bound by memory: 32768 x
-// 7168 bf16 230 us, 6.1 TB/s of 1.41 GB; the register form, whose loads wait for each row's sums, took 462.
+// 7168 bf16 233 us, 6.0 TB/s of 1.41 GB; the register form, whose loads wait for each row's sums, took 462.
 constexpr int kRingMost = 8;
 constexpr int kRingSm = 228 * 1024;            // shared memory of an SM, of which a block costs 1 KB and its own variables
 constexpr int kRingFixed = 2 * kRingMost * 8;  // full[kRingMost], empty[kRingMost]
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 }
 
 // dweight[h], dbias[h]: the blocks' partial sums added in a fixed order.  A block owns 32 columns; its 32
-// warps take the partials round robin, and their sums are added in a fixed tree.  304 blocks of 7168 columns: 10 us.
+// warps take the partials round robin, and their sums are added in a fixed tree.  304 blocks of 7168 columns: 9 us.
 __global__ void __launch_bounds__(1024) norm_param_kernel(const float* __restrict__ part, float* __restrict__ dweight,
                                                          float* __restrict__ dbias, int blocks, int H) {
   pdl_wait();
@@ -526,7 +526,7 @@ cudaError_t bwd_ring_launch(const moe_layernorm_config& c, const RingShape& r, c
 }
 
 // A warp holds rows of up to 128 packs (one pack a thread, or four: the register form of 32768 x 7168 took 462 us, the
-// ring 230, but the ring's threads would stand idle below).  Wider rows of 16-byte packs go through the ring of shared memory where a block
+// ring 233, but the ring's threads would stand idle below).  Wider rows of 16-byte packs go through the ring of shared memory where a block
 // has threads for them and three places (H up to 14336 in 16 bits, 7680 in fp32); the others stay in a block's
 // registers.
 template <class T, class P, int VEC>
