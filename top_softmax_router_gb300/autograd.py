@@ -9,6 +9,8 @@ VocabCE directly.)
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from .api import MoEBlock
@@ -20,6 +22,37 @@ from .scores import ScoreRouter
 
 __all__ = ["MoEFunction", "VocabCEFunction", "moe_block", "vocab_cross_entropy", "moe_experts", "expert_scores",
            "layer_norm", "token_embedding", "vocab_distill"]
+
+
+class _Final(torch.autograd.Function):
+    """The gradients as they are; differentiating them raises."""
+
+    @staticmethod
+    def forward(ctx, _anchor, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the library's gradients cannot be differentiated twice")
+
+
+def _once(backward):
+    """A backward pass that the library computes, without a graph.  Under create_graph its gradients would pass for
+    constants; they raise instead, also where the upstream gradient is one (torch's once_differentiable lets those by)."""
+
+    @functools.wraps(backward)
+    def run(ctx, *upstream):
+        with torch.no_grad():
+            grads = backward(ctx, *upstream)
+        if not torch.is_grad_enabled():
+            return grads
+        anchor = next((t for t in (*upstream, *ctx.saved_tensors) if t is not None and t.requires_grad), None)
+        if anchor is None:
+            return grads
+        final = iter(_Final.apply(anchor, *(g for g in grads if g is not None)))
+        return tuple(None if g is None else next(final) for g in grads)
+
+    return run
 
 
 class MoEFunction(torch.autograd.Function):
@@ -35,6 +68,7 @@ class MoEFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @_once
     def backward(ctx, dY):
         X, Wr, Wg, Wu, Wd, idx, gates = ctx.saved_tensors
         g = ctx.blk.backward(X, Wr, idx, gates, Wg, Wu, Wd, dY.contiguous(), want_dgates=False)
@@ -57,6 +91,7 @@ class VocabCEFunction(torch.autograd.Function):
         return mean[0]
 
     @staticmethod
+    @_once
     def backward(ctx, dmean):
         X, W, targets, lse = ctx.saved_tensors
         n = X.shape[0]
@@ -78,6 +113,7 @@ class _Experts(torch.autograd.Function):
         return blk.forward(X, idx, gates, Wg, Wu, Wd)
 
     @staticmethod
+    @_once
     def backward(ctx, dY):
         X, idx, gates, Wg, Wu, Wd = ctx.saved_tensors
         g = ctx.blk.experts_backward(X, idx, gates, Wg, Wu, Wd, dY.contiguous())
@@ -100,6 +136,7 @@ class _Scores(torch.autograd.Function):
         return idx, weights, counts
 
     @staticmethod
+    @_once
     def backward(ctx, _idx, dweights, _counts):
         logits, idx = ctx.saved_tensors
         return ctx.router.backward(logits, idx, dweights.contiguous()), None, None
@@ -125,6 +162,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -146,6 +184,7 @@ class _Embedding(torch.autograd.Function):
         return unit.forward(ids, table)
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         ids, = ctx.saved_tensors
         return None, ctx.unit.backward(ids, _dense_rows(dy)).to(ctx.type), None
@@ -165,6 +204,7 @@ class _Distill(torch.autograd.Function):
         return mean[0]
 
     @staticmethod
+    @_once
     def backward(ctx, dmean):
         X, W, ids, teacher, lse = ctx.saved_tensors
         n = X.shape[0]
