@@ -267,3 +267,17 @@ def test_other_stream_and_graph(M):
     graph.replay()
     assert all(torch.equal(p, q) for p, q in zip(ref, got))
     kd.check()
+
+
+@pytest.mark.parametrize("T", [1.0, 0.5, 0.25])
+def test_lowest_teacher_logits_at_low_temperatures(M, T):
+    """Entries so far below the row's largest that their distance, or that over T, is beyond fp32: their q is 0."""
+    X, W, ids, t, g = make(70, 64, 400, 9, seed=13)
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    t[::2, 3:] = low
+    t[5] = low
+    t[7, 1] = torch.finfo(torch.bfloat16).min
+    t[9, 0], t[9, 4] = high, low
+    out = run(M, X, W, ids, t, g, T=T)
+    assert all(torch.isfinite(v).all() for v in out)
+    compare(out, X, W, ids, t, g, T)

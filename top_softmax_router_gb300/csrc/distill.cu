@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(1024) distill_prep_kernel(const int32_t* __res
       const float e = there ? expf(x) : 0.0f;
       s_q[j] = e;
       sum += e;
-      dot = fmaf(e, x, dot);
+      if (e != 0.0f) dot = fmaf(e, x, dot);   // x may be -inf: a finite logit whose distance from m, over T, is past fp32
     }
     sum = warp_sum(sum);
     dot = warp_sum(dot);
