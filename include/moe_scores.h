@@ -27,8 +27,10 @@
  *   - logits [N, E] have a row stride ld (elements, >= E) and one of the MOE_TYPE_* types; dlogits is
  *     dense and of the same type.  bias and weights are fp32.
  *   - logits may be -inf (an expert that is masked for a token): its score is 0, it is chosen only when
- *     nothing else is left, with weight 0; a row of -inf alone has weights and gradients 0.  A bias may
- *     be -inf.  A NaN ranks below every number; the weights it reaches are NaN.
+ *     nothing else is left, with weight 0; a row of -inf alone has weights and gradients 0.  Scores
+ *     below fp32's range still share out the renormalised weights; a sigmoid logit below -709, whose
+ *     score is 0 in fp64 too, counts as -inf there.  A bias may be -inf.
+ *     A NaN ranks below every number; the weights it reaches are NaN.
  *   - backward: an index outside [0, E) is reported as MOE_ERR_DEVICE_CHECK through the workspace status
  *     word (moe_check_status) and takes no part; the k indices of a row are distinct.
  *   - shapes: N >= 0; 1 <= E <= 1024; groups divides E, 1 <= groups <= 32; 1 <= topk_groups <= groups;

@@ -213,3 +213,20 @@ def test_other_stream_and_graph(M):
     for _ in range(2):
         g.replay()
     assert all(torch.equal(p, q) for p, q in zip(ref, got))
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("E,groups", [(24, 1), (64, 8)])
+def test_sigmoid_logits_far_below_zero(M, renormalize, biased, E, groups):
+    """Scores below fp32's range: renormalised weights are shares of exp(l) there, and the gradient is theirs."""
+    l = logits_of(18, E, seed=11, std=3.0)
+    l += torch.tensor([-20.0, -60, -85, -95, -105, -200, -600, -690, 0])[:, None].repeat(2, 1)
+    l[9:, ::2] = -float("inf")                       # half the experts masked
+    l[17] = -float("inf")
+    l[17, [1, 5, 9]] = torch.tensor([-100.0, -101.5, 0.5])
+    kw = dict(groups=groups, topk_groups=max(1, groups // 2), score="sigmoid", renormalize=renormalize, scale=2.5)
+    _, w, _, _ = check(M, l, bias_of(E) if biased else None, 4, **kw)
+    if renormalize and not biased:
+        total = w[:17].double().sum(dim=1)
+        assert (total - 2.5).abs().max() <= 2.5 * 40 * U

@@ -52,12 +52,15 @@ __device__ __forceinline__ float rcp_approx(float x) {    // PTX rcp.approx: rel
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Below -64 the sigmoid is exp(l) to fp32, and exp(-l) would overflow.
+__device__ __forceinline__ float sigmoid_of(float l) { return l < -64.0f ? expf(l) : 1.0f / (1.0f + expf(-l)); }
+
 // What a row's scores are computed from: l -> s.
 struct RowScore {
   float m, sum, inv;   // softmax: maximum, sum of exp(l - m), 1 / sum
   bool sigmoid;
   __device__ __forceinline__ float of(float l) const {
-    if (sigmoid) return 1.0f / (1.0f + expf(-l));
+    if (sigmoid) return sigmoid_of(l);
     if (m == -INFINITY) return l == l ? 0.0f : l;
     return expf(l - m) / sum;
   }
@@ -80,6 +83,15 @@ __device__ __forceinline__ float chosen_exp(float l, float m) {
   if (l == -INFINITY) return 0.0f;
   const float d = l - m, b = d - l, off = (l - (d - b)) - (m + b);
   return expf(d) * (1.0f + off);
+}
+// A chosen expert's part of the sum that weights are renormalised by, up to a factor that all lanes share (l is -inf in
+// a lane without one).  A sigmoid of 0 or more is at least 1/2, and the scores are summed as they are; where every one
+// is smaller they are taken relative to the largest, as for the softmax, since fp32 holds none below exp(-104).
+__device__ __forceinline__ float chosen_part(float l, bool sigmoid) {
+  if (sigmoid && __any_sync(kFull, l >= 0.0f)) return sigmoid_of(l);
+  if (sigmoid && l < -709.0f) l = -INFINITY;   // 0 in fp64 too: a mask
+  const float e = chosen_exp(l, key_value(__reduce_max_sync(kFull, order_key(l))));
+  return sigmoid ? e / (1.0f + expf(l)) : e;
 }
 
 // fp64 scores of a row, for values that fp32 cannot order.
@@ -477,13 +489,11 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
     // weights; a lane without a slot adds 0
     const float ls = lane < p.k ? to_f32<T>(lr[my_e]) : -INFINITY;
     float s = 0.0f, total = 1.0f;
-    if (p.sigmoid || !p.renormalize) {
-      if (lane < p.k) s = score.of(ls);
-    } else {
-      s = chosen_exp(ls, key_value(__reduce_max_sync(kFull, order_key(ls))));   // the row's sum cancels
-    }
     if (p.renormalize) {
+      s = chosen_part(ls, p.sigmoid);
       total = warp_sum(s);
+    } else if (lane < p.k) {
+      s = score.of(ls);
     }
     if (lane < p.k) {
       topk_idx[row * p.k + lane] = my_e;
@@ -546,20 +556,16 @@ __global__ void __launch_bounds__(32 * kWarps) scores_bwd_kernel(const T* __rest
       for (int i = lane; i < E; i += 32) out[i] = -out[i] * inv * all;
     } else {
       for (int i = lane; i < E; i += 32) out[i] = 0.0f;
-      float s, rest;   // share of the renormalised sum (or the score), and the derivative's other factor
-      if (p.sigmoid) {
-        s = ok ? 1.0f / (1.0f + expf(-l)) : 0.0f;
-        rest = ok ? 1.0f / (1.0f + expf(l)) : 0.0f;
-      } else {   // renormalised softmax: a softmax over the chosen logits alone
-        const float m = key_value(__reduce_max_sync(kFull, order_key(ok ? l : -INFINITY)));
-        s = chosen_exp(l, m);   // l is -inf where there is no expert
-        rest = 1.0f;
-      }
+      // the derivative's factor beside the share of the renormalised sum (or the score)
+      const float rest = !p.sigmoid ? 1.0f : ok ? 1.0f / (1.0f + expf(l)) : 0.0f;
+      float s;
       if (p.renormalize) {
+        s = chosen_part(l, p.sigmoid);   // l is -inf where there is no expert
         const float total = warp_sum(s);
         s = total == 0.0f ? 0.0f : s / total;
         dl = p.scale * s * (dw - warp_sum(dw * s)) * rest;
-      } else {
+      } else {   // a sigmoid
+        s = ok ? sigmoid_of(l) : 0.0f;
         dl = p.scale * s * dw * rest;
       }
     }
