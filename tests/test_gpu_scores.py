@@ -230,3 +230,13 @@ def test_sigmoid_logits_far_below_zero(M, renormalize, biased, E, groups):
     if renormalize and not biased:
         total = w[:17].double().sum(dim=1)
         assert (total - 2.5).abs().max() <= 2.5 * 40 * U
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 8), (40, 4), (256, 32)])
+def test_group_scores_of_large_biases_that_cancel(M, score, E, groups):
+    """The group's first expert has a bias of 1000, the others of -1000: a group's score is what is left of their sum."""
+    b = torch.full((E,), -1000.0)
+    b[::E // groups] = 1000.0
+    l = logits_of(3000, E, seed=12, std=0.05)
+    check(M, l, b, 3, groups=groups, topk_groups=groups // 2, score=score)

@@ -125,9 +125,9 @@ __device__ __noinline__ double exact_value(const ExactScore x, const T* lr, cons
 }
 
 // The group's score from the values c[0 .. size) of its experts, spread over `width` lanes (a power of two):
-// the sum of its `top` largest.  NaN values are passed over.
+// the sum of its `top` largest, and *mass the sum of their absolute values.  NaN values are passed over.
 template <class F>
-__device__ __forceinline__ F group_score(const F* c, int size, int sub, int width, int top) {
+__device__ __forceinline__ F group_score(const F* c, int size, int sub, int width, int top, F* mass) {
   F m1 = (F)-INFINITY, m2 = (F)-INFINITY;
   for (int i = sub; i < size; i += width) {
     const F v = c[i];
@@ -141,7 +141,9 @@ __device__ __forceinline__ F group_score(const F* c, int size, int sub, int widt
     m1 = hi;
     m2 = lo > second ? lo : second;
   }
-  const F s = top == 2 && size > 1 ? m1 + m2 : m1;
+  const bool two = top == 2 && size > 1;
+  const F s = two ? m1 + m2 : m1;
+  *mass = fabs(m1) + (two ? fabs(m2) : (F)0);
   return s == s ? s : (F)-INFINITY;
 }
 
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
       const float wide = biased || by_score ? 8.0f * score.off() : 0.0f;
       const int g = lane / width, sub = lane % width;
       const bool mine = g < p.groups;
-      float gs;
+      float gs, mass;   // mass: what the two values' roundings are relative to, also where the values cancel
       if constexpr (RUN) {
         uint32_t k1 = 1u, k2 = 1u;   // the two largest keys
         if (by_score) {
@@ -298,7 +300,9 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
           k1 = max(k1, o1);
         }
         const float v1 = k1 > 1u ? key_value(k1) : -INFINITY, v2 = k2 > 1u ? key_value(k2) : -INFINITY;
-        gs = p.group_top == 2 && p.group_size > 1 ? v1 + v2 : v1;
+        const bool two = p.group_top == 2 && p.group_size > 1;
+        gs = two ? v1 + v2 : v1;
+        mass = fabsf(v1) + (two ? fabsf(v2) : 0.0f);
         if (gs != gs) gs = -INFINITY;
       } else {
         float* v32 = reinterpret_cast<float*>(vals);
@@ -307,9 +311,9 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
         for (int q = 0; q < PER; ++q)
           if (held(q)) v32[expert(q)] = by_score ? s_q[q] : key[q] > 1u ? key_value(key[q]) : NAN;
         __syncwarp();
-        gs = group_score<float>(v32 + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+        gs = group_score<float>(v32 + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top, &mass);
       }
-      const float w = wide + fabsf(gs) * (wide > 0.0f ? 0x1p-21f : 0.0f);
+      const float w = wide + mass * (wide > 0.0f ? 0x1p-21f : 0.0f);
       // rank of the group: how many are surely before it, and how many may be
       int before = 0, sure = 0, maybe = 0;
 #pragma unroll 4
@@ -330,7 +334,8 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
           __syncwarp();
           for (int e = lane; e < E; e += 32) vals[e] = exact_value<T>(exact, lr, p.bias, e);
           __syncwarp();
-          gd = group_score<double>(vals + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top);
+          double md;
+          gd = group_score<double>(vals + (mine ? g : 0) * p.group_size, p.group_size, sub, width, p.group_top, &md);
         }
         before = 0;
         for (int h = 0; h < p.groups; ++h) {
