@@ -9,7 +9,8 @@
  *   loss[n]  = T^2 sum_j q[n, j] (log q[n, j] - z[n, id[n, j]] + lse[n])       (KL, scaled by T^2)
  *   and, for an upstream gradient g[n] of loss[n],
  *   d[n, v]  = g[n] T (exp(z[n, v] - lse[n]) - sum over j with id[n, j] = v of q[n, j])   (stored in bf16,
- *              relative to g[0] T)
+ *              relative to T times the first g whose size is 2^-30 to 2^30, or to T where there is none:
+ *              where all rows have one gradient, or 0, that factor is not rounded)
  *   dX[n]    = sum_v d[n, v] W[v]    (fp32 accumulation, stored bf16)
  *   dW[v]    = sum_n d[n, v] X[n]    (fp32 accumulation, stored bf16 or fp32)
  *

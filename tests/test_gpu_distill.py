@@ -281,3 +281,17 @@ def test_lowest_teacher_logits_at_low_temperatures(M, T):
     out = run(M, X, W, ids, t, g, T=T)
     assert all(torch.isfinite(v).all() for v in out)
     compare(out, X, W, ids, t, g, T)
+
+
+@pytest.mark.parametrize("first", [0.0, 1.0])
+def test_one_gradient_for_all_rows_but_a_masked_first(M, first):
+    """One gradient g for all rows, the first of which may be masked.  p is 2^-8 within 10 % (logits of 0.02), so that p - 1
+    is a bf16 value within 4e-4, and g (1 - 2^-8) lies 0.95 of half a step from the next one: rounded as it is, every
+    d would be 3.7e-3 off the same way.  Relative to g, d is off by 4e-4 at its entry, and by 2^-8 of p elsewhere, whose
+    share of dW is sqrt(512) 2^-8 against 1 or more of the entries: 4e-4 + 0.09 x 2^-8, 8e-4."""
+    X, W, ids, t, _ = make(512, 64, 256, 1, seed=14, std=0.02)
+    g = torch.full((512,), (1 + 0.95 * 2.0 ** -8) / (1 - 2.0 ** -8) * 2.0 ** -9)
+    g[0] *= first
+    dW = run(M, X, W, ids, t, g, dt=torch.float32)[4]
+    ref = R.distill(f64(X), f64(W), ids.numpy(), f64(t), 1.0, f64(g))[3]
+    assert np.linalg.norm(f64(dW) - ref) <= 8e-4 * np.linalg.norm(ref)

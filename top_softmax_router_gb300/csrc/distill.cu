@@ -46,6 +46,22 @@ __global__ void __launch_bounds__(1024) distill_prep_kernel(const int32_t* __res
   int* s_class = count + tiles + 1 + warp * 2 * K;
   float* s_q = reinterpret_cast<float*>(s_class + K);
   for (int i = threadIdx.x; i <= tiles; i += 1024) count[i] = 0;
+  float c0 = 1.0f;
+  if (coef) {
+    // d is stored relative to the first gradient of an ordinary size (a masked row's is 0), which the products'
+    // epilogues put back in fp32: with one gradient for all rows (a mean) its rounding would otherwise be the same in
+    // every d and not average out
+    for (int base = 0; base < N; base += 1024) {
+      const int i = base + threadIdx.x;
+      const float g = i < N ? fabsf(dloss[i]) : 0.0f;
+      const uint32_t found = __ballot_sync(0xffffffffu, g >= 0x1p-30f && g <= 0x1p30f);
+      if (lane == 0) scratch[warp] = found ? base + warp * 32 + __ffs(found) - 1 : N;
+      if (__syncthreads_or(found != 0)) break;
+    }
+    const int first = __reduce_min_sync(0xffffffffu, scratch[lane]);
+    if (first < N) c0 = dloss[first];
+    if (group == 0 && threadIdx.x == 0) *out_scale = c0 * T;
+  }
   __syncthreads();
   if (row < N) {                            // the same for the whole warp
     const int64_t base = (int64_t)row * K;
@@ -68,20 +84,14 @@ __global__ void __launch_bounds__(1024) distill_prep_kernel(const int32_t* __res
       const float e = there ? expf(x) : 0.0f;
       s_q[j] = e;
       sum += e;
-      if (e != 0.0f) dot = fmaf(e, x, dot);   // x may be -inf: a finite logit whose distance from m, over T, is past fp32
+      if (e != 0.0f) dot = fmaf(e, x, dot);   // a finite logit's distance from m, over T, may pass fp32: x is -inf
     }
     sum = warp_sum(sum);
     dot = warp_sum(dot);
     const bool some = sum != 0.0f;          // the largest entry's e is 1
     if (lane == 0) {
       qlogq[row] = some ? dot / sum - logf(sum) : 0.0f;
-      if (coef) {
-        // d is stored relative to the first row's gradient, which the products' epilogues put back in fp32: with one
-        // gradient for all rows (a mean) its rounding would otherwise be the same in every d and not average out
-        const float g0 = dloss[0], c = fabsf(g0) >= 0x1p-30f && fabsf(g0) <= 0x1p30f ? g0 : 1.0f;
-        coef[row] = some ? dloss[row] / c : 0.0f;
-        if (row == 0) *out_scale = c * T;
-      }
+      if (coef) coef[row] = some ? dloss[row] / c0 : 0.0f;
     }
     __syncwarp();
     for (int j = lane; j < K; j += 32) {
