@@ -17,6 +17,8 @@
  *     only their element's alignment: rows that are 16-byte aligned take 16-byte loads.
  *   - shapes: N >= 0, 1 <= H <= 16384.  Else MOE_ERR_UNSUPPORTED_SHAPE.  eps >= 0 and finite.
  *   - repeated calls on the same inputs give the same bits (every sum has a fixed order).
+ *   - a wait of the backward that runs out (moe_set_wait_limit_ns) is reported as MOE_ERR_TIMEOUT through
+ *     the workspace status word (moe_check_status); the call's gradients are then of no use.
  */
 #ifndef TOP_SOFTMAX_ROUTER_MOE_NORM_H_
 #define TOP_SOFTMAX_ROUTER_MOE_NORM_H_

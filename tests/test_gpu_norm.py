@@ -191,3 +191,15 @@ def test_other_stream_and_graph(M):
     g.replay()
     for p, q in zip(ref, got):
         assert torch.equal(p, q)
+
+
+def test_a_wait_that_ran_out_is_raised_by_check(M):
+    """The status that a timed-out wait leaves in the unit's workspace (here from the library's own diagnostic wait)."""
+    from top_softmax_router_gb300._lib import MoeError
+    ln = M.LayerNorm(M.LayerNormConfig(N=4, H=32))
+    ln.check()
+    M.diag_wait_timeout(1_000_000, ln.ws)
+    with pytest.raises(MoeError) as e:
+        ln.check()
+    assert e.value.code == -5
+    ln.check()

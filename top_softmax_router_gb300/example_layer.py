@@ -87,7 +87,7 @@ class Layer:
         return loss.detach()
 
     def check(self):
-        for unit in (self.embed, self.router, self.block, self.distill):
+        for unit in (self.embed, self.norm, self.router, self.block, self.distill):
             unit.check()
 
 

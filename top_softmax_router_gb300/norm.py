@@ -87,3 +87,8 @@ class LayerNorm:
             self.ws.data_ptr(), self.ws.numel(), on.handle), "moe_layernorm_backward")
         on.uses(x, weight, mean, rstd, dy, self.ws)
         return dx, dw, db
+
+    def check(self, stream=None) -> None:
+        """Raises if a wait of a backward since the last check ran out: its gradients are then of no use."""
+        from .api import check_status
+        check(check_status(self.ws, stream), "device status")
