@@ -37,3 +37,23 @@ def test_bad_expert_id_is_reported_not_faulted():
     off = torch.empty(K, 5, dtype=torch.int32, device="cuda")
     M.plan(cfg, idx, rr, ro, off, ws)
     assert M.check_status(ws) == _lib.MOE_ERR_DEVICE_CHECK
+
+
+def test_a_norm_whose_waits_may_run_out_leaves_the_context_usable():
+    """A wait limit far below a copy's time: the backward either ends as ever or reports the timeout, and the next call,
+    under the usual limit, gives the usual bits."""
+    need_gpu()
+    M = lib_api()
+    from top_softmax_router_gb300 import _lib
+    x, dy = (torch.randn(3000, 7168, device="cuda").bfloat16() for _ in range(2))
+    ln = M.LayerNorm(M.LayerNormConfig(N=3000, H=7168))
+    _, mean, rstd = ln.forward(x)
+    want = ln.backward(x, None, mean, rstd, dy)
+    M.set_wait_limit_ns(1000)
+    try:
+        ln.backward(x, None, mean, rstd, dy)
+        assert M.check_status(ln.ws) in (0, _lib.MOE_ERR_TIMEOUT)
+    finally:
+        M.set_wait_limit_ns(0)
+    assert all(torch.equal(p, q) for p, q in zip(want, ln.backward(x, None, mean, rstd, dy)))
+    ln.check()

@@ -156,6 +156,10 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   }
 }
 
+// Far longer than a copy or an MMA that has been issued takes: how long a block whose wait ran out stays for them at
+// least, whatever the wait limit is.
+constexpr int64_t kSettleNs = 200000;
+
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

@@ -260,7 +260,7 @@ struct Ring {
       uint32_t ph = phase;
       if (s < 0) s += stages, ph ^= 1u;
       volatile int no_abort = 0;
-      wait_bounded(full(s), ph, &no_abort, limit_ns, nullptr, 0);
+      wait_bounded(full(s), ph, &no_abort, max(limit_ns, kSettleNs), nullptr, 0);
     }
   }
 };
@@ -350,14 +350,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     for (int j = 0; j < PAIRS; ++j) gw[i][j] = gb[i][j] = f32x2(0.0f);
   int stage = 0, it = 0;
   uint32_t phase = 0;
+  bool good = true;   // lane 0: no wait has run out
   float mu = 0.0f, rs = 0.0f;
   if ((int)blockIdx.x < N) mu = mean[blockIdx.x], rs = rstd[blockIdx.x];
   for (int64_t row = blockIdx.x; row < N; row += gridDim.x, ++it) {
     const int64_t next = row + gridDim.x;
     float mu_next = 0.0f, rs_next = 0.0f;
     if (next < N) mu_next = mean[next], rs_next = rstd[next];
-    // after a wait that ran out the sums are of no use (the status says so); every warp still meets the others below
-    if (lane == 0) wait_bounded(ring.full(stage), phase, ring.abort_flag, limit_ns, status, 803);
+    // After a wait that ran out the sums are of no use (the status says so), and no place is given back: its copies may
+    // still be on their way.  Every warp still meets the others below.
+    if (lane == 0) good &= wait_bounded(ring.full(stage), phase, ring.abort_flag, limit_ns, status, 803);
     __syncwarp();
     const T* at = reinterpret_cast<const T*>(places + (size_t)stage * 2 * row_bytes);
     f32x2 s2(0.0f), sx2(0.0f);
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(ring.empty(stage));
+    if (lane == 0 && good) mbar_arrive(ring.empty(stage));
     if (++stage == stages) stage = 0, phase ^= 1u;
     mu = mu_next;
     rs = rs_next;
