@@ -57,3 +57,28 @@ def test_a_norm_whose_waits_may_run_out_leaves_the_context_usable():
         M.set_wait_limit_ns(0)
     assert all(torch.equal(p, q) for p, q in zip(want, ln.backward(x, None, mean, rstd, dy)))
     ln.check()
+
+
+def test_a_head_whose_waits_may_run_out_leaves_the_context_usable():
+    """The same for the distillation head's products."""
+    need_gpu()
+    M = lib_api()
+    from top_softmax_router_gb300 import _lib
+    N, H, V, K = 520, 2112, 5000, 4
+    X, W = torch.randn(N, H, device="cuda").bfloat16(), torch.randn(V, H, device="cuda").mul(H ** -0.5).bfloat16()
+    ids = torch.randint(0, V, (N, K), device="cuda", dtype=torch.int32)
+    t, g = torch.randn(N, K, device="cuda"), torch.full((N,), 1 / N, device="cuda")
+    kd = M.VocabDistill(M.DistillConfig(N=N, H=H, V=V, K=K))
+    want = kd.forward(X, W, ids, t)
+    want += kd.backward(X, W, ids, t, want[1], g)
+    M.set_wait_limit_ns(1000)
+    try:
+        kd.forward(X, W, ids, t)
+        kd.backward(X, W, ids, t, want[1], g)
+        assert M.check_status(kd.ws) in (0, _lib.MOE_ERR_TIMEOUT)
+    finally:
+        M.set_wait_limit_ns(0)
+    again = kd.forward(X, W, ids, t)
+    again += kd.backward(X, W, ids, t, again[1], g)
+    assert all(torch.equal(p, q) for p, q in zip(want, again))
+    kd.check()

@@ -313,6 +313,13 @@ __device__ __forceinline__ void head_tile(const HeadGemm& p, int w, int* mt, int
   *mt = b * p.band + (rem - *nt * in_band);
 }
 
+// A wait ran out: the copies in flight (this CTA's and the peer's) complete on the even CTA's barriers in an order that no
+// longer says when the last one has landed, so both CTAs stay (they leave together) for far longer than a copy takes.
+__device__ __forceinline__ void head_settle() {
+  const uint64_t t0 = globaltimer();
+  while ((int64_t)(globaltimer() - t0) < kSettleNs) {}
+}
+
 // A_MN / B_MN: the operand lies with its rows along K ([K][M] or [K][N] in memory).
 template <int EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
@@ -399,12 +406,7 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
         }
       }
       pdl_trigger();                                // every load is issued: the next kernel may be scheduled
-      if (!ok) {
-        // A wait ran out: the copies in flight (this CTA's and the peer's) complete on the even CTA's barriers in an
-        // order that no longer says when the last one has landed, so both CTAs stay for far longer than a copy takes.
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 200000) {}
-      }
+      if (!ok) head_settle();
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -458,7 +460,8 @@ __global__ void __launch_bounds__(HeadSmem::THREADS, 1)
       if (lane == 0) {                              // every MMA has completed before the tensor memory is freed
         tc_commit_pair(drain_bar, 0x1);
         volatile int no_abort = 0;
-        wait_bounded(drain_bar, 0, &no_abort, p.limit_ns, nullptr, 0);
+        wait_bounded(drain_bar, 0, &no_abort, max(p.limit_ns, kSettleNs), nullptr, 0);
+        if (!ok) head_settle();                     // the loads it gave up on, which may all have been issued
       }
       __syncwarp();
     }
