@@ -203,3 +203,17 @@ def test_a_wait_that_ran_out_is_raised_by_check(M):
         ln.check()
     assert e.value.code == -5
     ln.check()
+
+
+@pytest.mark.parametrize("t,pt,n,h", [("bf16", "fp32", 6000, 1032), ("fp32", "fp32", 6000, 1024), ("bf16", "bf16", 3000, 7168),
+                                      ("fp16", "fp16", 2500, 4096), ("fp32", "fp32", 1300, 7680), ("bf16", "bf16", 1100, 14336),
+                                      ("fp32", "fp32", 2500, 1001), ("bf16", "bf16", 1300, 8200), ("fp32", "fp32", 700, 8192),
+                                      ("bf16", "fp32", 500, 16384), ("bf16", "fp32", 700, 4101), ("fp16", "fp16", 2600, 300),
+                                      ("bf16", "bf16", 600, 2051), ("bf16", "fp32", 3000, 1000)])
+def test_many_rows_of_each_form(M, t, pt, n, h):
+    """Every form of the backward with more rows a block than it holds at a time (the ring: than it has places)."""
+    a = inputs(n, h, t, pt, seed=n + h)
+    unit = M.LayerNorm(M.LayerNormConfig(N=n, H=h))
+    first = check(M, *a, unit=unit)
+    again = check(M, *a, unit=unit)
+    assert all(torch.equal(p, q) for p, q in zip(first, again))
