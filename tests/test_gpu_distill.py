@@ -295,3 +295,14 @@ def test_one_gradient_for_all_rows_but_a_masked_first(M, first):
     dW = run(M, X, W, ids, t, g, dt=torch.float32)[4]
     ref = R.distill(f64(X), f64(W), ids.numpy(), f64(t), 1.0, f64(g))[3]
     assert np.linalg.norm(f64(dW) - ref) <= 8e-4 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("N,H,V,K,P,T", [(70, 1088, 600, 5, 1, 1.0), (33, 2048, 513, 8, 1, 2.0), (130, 2112, 1000, 3, 2, 1.0),
+                                         (40, 4096, 700, 16, 1, 4.0), (260, 2112, 10300, 4, 1, 1.0), (520, 1152, 9001, 6, 1, 2.0)])
+def test_logits_of_several_accumulators(M, N, H, V, K, P, T):
+    """More than 1024 products a logit: two to four accumulators a tile, the last one short, an odd number of them
+    carried from tile to tile where there are more tiles than clusters (the last two cases: 82 and 108 tiles)."""
+    a = make(N, H, V, K, seed=H + V)
+    out = run(M, *a, P=P, T=T)
+    compare(out, *a, T)
+    assert all(torch.equal(p, q) for p, q in zip(out, run(M, *a, P=P, T=T)))
