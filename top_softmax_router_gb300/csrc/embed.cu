@@ -340,9 +340,8 @@ __device__ __forceinline__ int lower_bound_warp(const uint32_t* keys, int n, uin
   return lo;
 }
 
-// a[k][j] += sum over i < n of dy[order[i]][c + k step + j], in order, eight rows' loads at a time.
-// a[k][j] += sum over i < n of dy[order[i]][c + k step + j] for the PACKS packs below H, in order, eight rows' loads at a
-// time.
+// a[k][j] += sum over i < n of dy[order[i]][c + k step + j] for the PACKS packs below H, in order, eight rows'
+// loads at a time.
 template <int PACKS, class T, int VEC>
 __device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t lddy, const int* order, int n, int c, int step,
                                          int H, float (&a)[PACKS][VEC]) {

@@ -9,9 +9,11 @@
 // Warps of a CTA (320 threads): 0 loads, 1 issues the MMAs (even CTA), 2..9 are the epilogue: two for each quarter of
 // the tensor memory's lanes, one for each half of the tile's columns.
 //
-// Bound by the tensor cores at size (8192 x 4096 x 65536, 4.4 TFLOP each: logits 2.85 ms, 1.54 PFLOP/s; d 2.72; dX 2.80;
-// dW 2.83, under the power cap), by whole waves of tiles on 76 clusters below (2048 x 1024 x 32000: logits 104 us, 1.29
-// PFLOP/s), and by launch and load latency where there are few tiles (300 x 128 x 1000: 10 to 14 us each).
+// Bound by the tensor cores at size (8192 x 4096 x 65536, 4.4 TFLOP each, launches apart at 2070 MHz: logits 2.67 ms,
+// 1.65 PFLOP/s; d 2.53; dX 2.64; dW 2.64; in steps back to back the power cap leaves about 1730 MHz: 3.04, 2.85, 2.94,
+// 2.96). Below, by whole waves of tiles on 76 clusters and the tiles' own latency (2048 x 1024 x 32000: logits 103 us,
+// 1.3 PFLOP/s, the tensor pipe at work 54 % of the time; d, dX and dW 35 to 42 %), and by launch and load latency
+// where there are few tiles (300 x 128 x 1000: 10 to 14 us each).
 //
 // Every wait is bounded (wait_bounded): a wait that runs out sets the workspace status, and both CTAs leave.
 #pragma once
@@ -60,8 +62,10 @@ struct HeadGemm {
 // The tensor cores cut each addition to an accumulator off towards zero, so that a logit of H products comes out too
 // small, by up to H / 16 x 2^-24 of itself, the larger the logit the more, and lse with it (H = 4096: 1.5e-6 of lse,
 // against 5e-8 of fp32 sums).  The forward therefore sums 1024 products to an accumulator and adds those in fp32
-// registers: the accumulators stay small, and so does what is cut off (3.6e-7; 512 products: 1.7e-7, but the forward of
-// 8192 x 4096 x 65536 took 2903 us for 2689; unsplit 2579).  d is rounded to bf16 and is left alone.
+// registers: the accumulators stay small, and so does what is cut off (3.6e-7; 512 products: 1.7e-7, but the logits of
+// 8192 x 4096 x 65536 took 2903 us for 2689).  Unsplit they take 2580, in steps under the power cap 2930 for 3040: 4 %
+// either way.  The sums cost registers too: 168 a thread, and 136 bytes are spilled.  d is rounded to bf16 and is left
+// alone.
 constexpr int kLseShare = 16;
 
 struct HeadSmem {

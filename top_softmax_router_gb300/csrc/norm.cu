@@ -28,8 +28,9 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int tpr, float2* re
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-// Bound by memory: 32768 x 7168 bf16 with fp32 parameters 161 us, 5.8 TB/s of its 0.94 GB; 4099 x 1001 fp32, where a row
-// starts on no 16 bytes, 10 us.
+// Bound by memory: 32768 x 7168 bf16 with fp32 parameters 160 us, 5.9 TB/s of its 0.94 GB, with bf16 ones 149; 4099 x
+// 1001 fp32, where a row starts on no 16 bytes, 10 us.  With 16-bit parameters eight packs of eight spill 96 to 116
+// bytes.
 // One pass: x is read once, kept in registers for the mean, the variance around it and the output.  TPR threads a row
 // at compile time, so that the packs' addresses are constants from the thread's first; places past the row hold zeros
 // and are masked by data, not by branches (with both at run time the arithmetic of 32768 x 7168 held it at 195 us).
@@ -528,9 +529,12 @@ cudaError_t bwd_ring_launch(const moe_layernorm_config& c, const RingShape& r, c
 }
 
 // A warp holds rows of up to 128 packs (one pack a thread, or four: the register form of 32768 x 7168 took 462 us, the
-// ring 233, but the ring's threads would stand idle below).  Wider rows of 16-byte packs go through the ring of shared memory where a block
-// has threads for them and three places (H up to 14336 in 16 bits, 7680 in fp32); the others stay in a block's
-// registers.
+// ring 233, but the ring's threads would stand idle below): 262144 x 256 bf16 95 us, 4.2 TB/s; 262144 x 512, four
+// packs a thread and two blocks an SM, 414 us, 1.9 TB/s.  Wider rows of 16-byte packs go through the ring of shared
+// memory where a block has threads for them and three places (H up to 14336 in 16 bits, 7680 in fp32); the others stay
+// in a block's registers.  Those of 1024 threads have 64 each, spill 672 to 1574 bytes and are far from memory's rate:
+// 16384 x 8192 fp32 1070 us, where 7680 columns take 254 through the ring; 16384 x 16384 bf16 4276; 32768 x 7169 bf16,
+// by single elements, 4726.
 template <class T, class P, int VEC>
 cudaError_t bwd_shape(const moe_layernorm_config& c, const void* x, int64_t ldx, const void* weight, const float* mean,
                       const float* rstd, const void* dy, int64_t lddy, void* dx, float* part, int* blocks, int* status,

@@ -172,10 +172,11 @@ __device__ __noinline__ double group_score_run(const ExactScore x, const T* lr, 
 // values can be in the wrong order only if they lie within `window` of each other; where that happens among the
 // candidates they are compared in fp64 (unless their logit and bias are equal, when the tie rule decides).
 
-// Bound by its arithmetic, about 1100 instructions a row of 384: 32768 x 384 with 8 groups, k = 8 53 us (the logits
-// alone are 7.4 us of memory), 35 us without groups; 16384 x 64 13 us.
-// Blocks an SM.
-constexpr int fwd_blocks(int per) { return per <= 4 ? 4 : per <= 12 ? 4 : per <= 16 ? 2 : 1; }
+// Bound by its arithmetic: 32768 x 384 with 8 groups, k = 8 takes 1102 instructions a row, 75 of them loads and stores
+// of spilled registers, 55 us (the logits alone are 7.4 us of memory); 16384 x 64 483 a row, 13 us, of which their
+// issue is 6 and the rest latency: a warp has three or four rows.
+// Blocks an SM (four leave 64 registers a thread, and the forms of up to 12 experts a lane spill 48 to 276 bytes).
+constexpr int fwd_blocks(int per) { return per <= 12 ? 4 : per <= 16 ? 2 : 1; }
 
 // RUN: lane t holds the PER = E / 32 consecutive experts from t PER on, so that a lane's experts are of one group and the
 // groups are scored in registers.  Else lane t holds experts t, t + 32, .. and the groups are scored from shared memory.
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(32 * kWarps, fwd_blocks(PER))
   }
 }
 
-// 32768 x 384 fp32: 18 us for the 50 MB it writes (half of them still in L2 when it ends).
+// 32768 x 384 fp32: 19 us for the 50 MB it writes (half of them still in L2 when it ends), 312 instructions a row.
 // One warp a row: the chosen experts' gradients (and, for a softmax that is not renormalised, everyone's) are
 // put together in shared memory and the row is stored whole.
 template <class T, int VEC>
