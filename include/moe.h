@@ -272,7 +272,8 @@ enum {
   MOE_K_CE_LOGITS, MOE_K_CE_MERGE, MOE_K_CE_DLOGIT, MOE_K_CE_DX, MOE_K_CE_DW, MOE_K_ROUTE_GRAD,
   MOE_K_NORM_FWD, MOE_K_NORM_BWD, MOE_K_EMBED_FWD, MOE_K_EMBED_SORT, MOE_K_EMBED_BWD, MOE_K_SCORES_FWD,
   MOE_K_SCORES_BWD, MOE_K_DISTILL_PREP, MOE_K_DISTILL_LOGITS, MOE_K_DISTILL_LOSS, MOE_K_DISTILL_D, MOE_K_DISTILL_DX,
-  MOE_K_DISTILL_DW, MOE_K_COUNT
+  MOE_K_DISTILL_DW, MOE_K_BLOCKS8, MOE_K_LINEAR_Y, MOE_K_LINEAR_DX, MOE_K_LINEAR_DW, MOE_K_RMS_FWD, MOE_K_RMS_BWD,
+  MOE_K_COUNT
 };
 
 /* When on, every kernel launch is bracketed by CUDA events on its stream. */

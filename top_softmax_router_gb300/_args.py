@@ -1,4 +1,5 @@
-"""Argument marshalling shared by the layer operators' bindings (norm.py, embed.py, scores.py, distill.py)."""
+"""Argument marshalling shared by the layer operators' bindings (norm.py, embed.py, scores.py, distill.py, rmsnorm.py,
+blocks8.py, linear.py)."""
 from __future__ import annotations
 
 import ctypes
@@ -58,6 +59,15 @@ def count(t, name: str, most: int) -> int:
     if n > most:
         raise ValueError(f"{name}: {n} rows, made for at most {most}")
     return n
+
+
+def here(device, *tensors):
+    """The tensors of a call lie on the unit's device, and that is the current one: the library launches there."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"expected tensors on {device}, got one on {t.device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"expected {device} to be the current device")
 
 
 class On:

@@ -26,7 +26,8 @@ KERNEL_CLASSES = ["router_logits", "router_topk", "plan", "gather", "gemm_gateup
                   "gemm_dact", "gemm_dw", "gemm_dx", "unpermute", "router_dw", "zero", "hop_plan", "finalize",
                   "adamw", "ce_logits", "ce_merge", "ce_dlogit", "ce_dx", "ce_dw", "route_grad", "norm_fwd",
                   "norm_bwd", "embed_fwd", "embed_sort", "embed_bwd", "scores_fwd", "scores_bwd", "distill_prep",
-                  "distill_logits", "distill_loss", "distill_d", "distill_dx", "distill_dw"]
+                  "distill_logits", "distill_loss", "distill_d", "distill_dx", "distill_dw", "blocks8", "linear_y",
+                  "linear_dx", "linear_dw", "rms_fwd", "rms_bwd"]
 
 # Every symbol include/*.h declares.
 EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "moe_forward", "moe_backward", "moe_experts_backward",
@@ -39,7 +40,9 @@ EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "mo
            "moe_layernorm_workspace_bytes", "moe_layernorm_forward", "moe_layernorm_backward",
            "moe_embed_workspace_bytes", "moe_embed_forward", "moe_embed_backward",
            "moe_scores_workspace_bytes", "moe_scores_forward", "moe_scores_backward",
-           "moe_distill_workspace_bytes", "moe_distill_forward", "moe_distill_backward"]
+           "moe_distill_workspace_bytes", "moe_distill_forward", "moe_distill_backward",
+           "moe_blocks8_pack", "moe_blocks8_unpack", "moe_blocks8_pack_weight",
+           "moe_linear_workspace_bytes", "moe_linear_forward", "moe_linear_backward"]
 
 MOE_GEMM_AUTO, MOE_GEMM_SINGLE, MOE_GEMM_PAIR = 0, 1, 2
 MOE_DISPATCH_GATHER, MOE_DISPATCH_ON_LOAD = 0, 1
@@ -79,6 +82,10 @@ class DistillConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "V", "K", "P")] + [("temperature", ctypes.c_float)]
 
 
+class LinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "O", "E", "blocks8")]
+
+
 class CeStats(ctypes.Structure):
     _fields_ = [("strips", ctypes.c_int32), ("strip_classes", ctypes.c_int32), ("strip_bytes", ctypes.c_int64),
                 ("strip_bound_bytes", ctypes.c_int64), ("partial_bytes", ctypes.c_int64),
@@ -111,7 +118,7 @@ def load() -> ctypes.CDLL:
         hpp = ctypes.POINTER(AdamwHparams)
         cep = ctypes.POINTER(CeConfig)
         lnp, emp, scp = ctypes.POINTER(LayerNormConfig), ctypes.POINTER(EmbedConfig), ctypes.POINTER(ScoresConfig)
-        dsp = ctypes.POINTER(DistillConfig)
+        dsp, lip = ctypes.POINTER(DistillConfig), ctypes.POINTER(LinearConfig)
         sig = {
             "moe_workspace_bytes": [cfgp, ctypes.POINTER(SZ), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
             "moe_route": [cfgp, P, P, P, P, P, P, SZ, P],
@@ -157,6 +164,12 @@ def load() -> ctypes.CDLL:
             "moe_distill_workspace_bytes": [dsp, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
             "moe_distill_forward": [dsp, P, P, P, P, P, P, P, P, SZ, P],
             "moe_distill_backward": [dsp, P, P, P, P, P, P, P, P, I32, P, SZ, P],
+            "moe_blocks8_pack": [P, I64, I32, I64, I32, P, P, P],
+            "moe_blocks8_unpack": [P, P, I64, I32, P, I32, P],
+            "moe_blocks8_pack_weight": [P, I32, I32, I32, I32, P, P, P],
+            "moe_linear_workspace_bytes": [lip, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
+            "moe_linear_forward": [lip, P, I64, P, P, P, P, P, P, SZ, P],
+            "moe_linear_backward": [lip, P, I64, P, P, P, P, P, P, P, I32, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)

@@ -197,6 +197,17 @@ bool make_map_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows
                  uint32_t box_inner, uint32_t box_rows);
 bool make_map_3d_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
                      uint32_t box_inner, uint32_t box_rows);
+// bytes (e4m3 codes); a box row is at most 128
+bool make_map_2d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride,
+                    uint32_t box_inner, uint32_t box_rows);
+bool make_map_3d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t depth,
+                    uint32_t box_inner, uint32_t box_rows);
+
+// 8-bit blocks (blocks8.cu): rows of x to codes [N][H] and scales [N][ceil(H / 128)], and back
+cudaError_t launch_pack_rows(const void* x, int64_t ldx, int type, int64_t N, int H, uint8_t* codes, uint8_t* scales,
+                             cudaStream_t s);
+cudaError_t launch_unpack_rows(const uint8_t* codes, const uint8_t* scales, int64_t N, int H, void* y, int type,
+                               cudaStream_t s);
 
 // helpers of the ABI layer (moe_api.cu) shared with the optimizer step (adamw.cu)
 int record_cuda_error(cudaError_t e, const char* what);  // keeps the message for moe_strerror; MOE_ERR_CUDA

@@ -61,7 +61,9 @@ const char* kKernelNames[MOE_K_COUNT] = {"router_logits", "router_topk", "plan",
                                          "ce_dw",         "route_grad",  "norm_fwd",  "norm_bwd",
                                          "embed_fwd",     "embed_sort",  "embed_bwd", "scores_fwd",
                                          "scores_bwd",    "distill_prep", "distill_logits", "distill_loss",
-                                         "distill_d",     "distill_dx",  "distill_dw"};
+                                         "distill_d",     "distill_dx",  "distill_dw", "blocks8",
+                                         "linear_y",      "linear_dx",   "linear_dw", "rms_fwd",
+                                         "rms_bwd"};
 
 cudaEvent_t take_event() {
   if (!g_free_events.empty()) {
