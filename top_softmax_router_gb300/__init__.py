@@ -7,6 +7,7 @@ from .adamw import *  # noqa: F401,F403
 from .ce import *  # noqa: F401,F403
 from .norm import *  # noqa: F401,F403
 from .blocks8 import *  # noqa: F401,F403
+from .rmsnorm import *  # noqa: F401,F403
 from .linear import *  # noqa: F401,F403
 from .embed import *  # noqa: F401,F403
 from .scores import *  # noqa: F401,F403

@@ -42,7 +42,8 @@ EXPORTS = ["moe_workspace_bytes", "moe_route", "moe_plan", "moe_chunk_plan", "mo
            "moe_scores_workspace_bytes", "moe_scores_forward", "moe_scores_backward",
            "moe_distill_workspace_bytes", "moe_distill_forward", "moe_distill_backward",
            "moe_blocks8_pack", "moe_blocks8_unpack", "moe_blocks8_pack_weight",
-           "moe_linear_workspace_bytes", "moe_linear_forward", "moe_linear_backward"]
+           "moe_linear_workspace_bytes", "moe_linear_forward", "moe_linear_backward",
+           "moe_rmsnorm_workspace_bytes", "moe_rmsnorm_forward", "moe_rmsnorm_backward"]
 
 MOE_GEMM_AUTO, MOE_GEMM_SINGLE, MOE_GEMM_PAIR = 0, 1, 2
 MOE_DISPATCH_GATHER, MOE_DISPATCH_ON_LOAD = 0, 1
@@ -86,6 +87,10 @@ class LinearConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "O", "E", "blocks8")]
 
 
+class RmsNormConfig(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 class CeStats(ctypes.Structure):
     _fields_ = [("strips", ctypes.c_int32), ("strip_classes", ctypes.c_int32), ("strip_bytes", ctypes.c_int64),
                 ("strip_bound_bytes", ctypes.c_int64), ("partial_bytes", ctypes.c_int64),
@@ -118,7 +123,7 @@ def load() -> ctypes.CDLL:
         hpp = ctypes.POINTER(AdamwHparams)
         cep = ctypes.POINTER(CeConfig)
         lnp, emp, scp = ctypes.POINTER(LayerNormConfig), ctypes.POINTER(EmbedConfig), ctypes.POINTER(ScoresConfig)
-        dsp, lip = ctypes.POINTER(DistillConfig), ctypes.POINTER(LinearConfig)
+        dsp, lip, rmp = ctypes.POINTER(DistillConfig), ctypes.POINTER(LinearConfig), ctypes.POINTER(RmsNormConfig)
         sig = {
             "moe_workspace_bytes": [cfgp, ctypes.POINTER(SZ), ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
             "moe_route": [cfgp, P, P, P, P, P, P, SZ, P],
@@ -167,6 +172,9 @@ def load() -> ctypes.CDLL:
             "moe_blocks8_pack": [P, I64, I32, I64, I32, P, P, P],
             "moe_blocks8_unpack": [P, P, I64, I32, P, I32, P],
             "moe_blocks8_pack_weight": [P, I32, I32, I32, I32, P, P, P],
+            "moe_rmsnorm_workspace_bytes": [rmp, ctypes.POINTER(SZ)],
+            "moe_rmsnorm_forward": [rmp, P, I64, P, I64, P, P, P, P, P, P, I32, I32, P],
+            "moe_rmsnorm_backward": [rmp, P, I64, P, P, P, I64, P, I64, P, P, I32, I32, P, SZ, P],
             "moe_linear_workspace_bytes": [lip, ctypes.POINTER(SZ), ctypes.POINTER(SZ)],
             "moe_linear_forward": [lip, P, I64, P, P, P, P, P, P, SZ, P],
             "moe_linear_backward": [lip, P, I64, P, P, P, P, P, P, P, I32, P, SZ, P],

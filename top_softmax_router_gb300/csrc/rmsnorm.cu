@@ -1,0 +1,404 @@
+// Root-mean-square norm with the residual's addition and an output in 8 bits (include/moe_rmsnorm.h).
+//
+// A half warp holds blocks of 128 columns of a row, eight values a lane, so that a block's largest magnitude is four
+// shuffles away: PER blocks a half warp, TPR threads a row (whole warps), several rows a block of threads where rows are
+// short.  Rows stay in registers between the statistics and the output: x, the residual and the outputs pass memory once.
+// Both kernels are persistent, and load their next row while they work on this one where the registers allow it.
+#include <algorithm>
+
+#include "../../include/moe_blocks8.h"
+#include "../../include/moe_rmsnorm.h"
+#include "blocks8.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxThreads = 512;
+
+// The sum over a row's threads (tpr of them, whole warps of row group `group`), in a fixed order, in every thread.  red
+// is taken in turn, so that one barrier a row suffices.
+__device__ __forceinline__ float row_sum(float v, int tpr, int group, float* red) {
+  v = warp_sum(v);
+  if (tpr == 32) return v;
+  const int warps = tpr >> 5, first = group * warps;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int i = 0; i < warps; ++i) v += red[first + i];
+  return v;
+}
+
+template <class T, bool VEC>
+__device__ __forceinline__ Pack<T, 8> load_raw8(const T* p, int lane16, int valid) {
+  Pack<T, 8> a = zero_pack<T, 8>();
+  if constexpr (VEC) {
+    if (lane16 * 8 < valid) a = load_pack<T, 8>(p + lane16 * 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane16 + 16 * i < valid) a.v[i] = p[lane16 + 16 * i];
+  }
+  return a;
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void store_raw8(T* p, int lane16, int valid, const Pack<T, 8>& a) {
+  if constexpr (VEC) {
+    if (lane16 * 8 < valid) store_pack<T, 8>(p + lane16 * 8, a);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane16 + 16 * i < valid) p[lane16 + 16 * i] = a.v[i];
+  }
+}
+
+// A thread's place in its row: block i of its half warp starts at column(i) and has valid(i) columns.
+struct RowPlace {
+  int group, rows, t, lane16, hw, hws, H;
+  __device__ __forceinline__ RowPlace(int tpr, int H_) : H(H_) {
+    rows = blockDim.x / tpr;
+    group = threadIdx.x / tpr;
+    t = threadIdx.x - group * tpr;
+    lane16 = t & 15;
+    hw = t >> 4;
+    hws = tpr >> 4;
+  }
+  __device__ __forceinline__ int block(int i) const { return hw + i * hws; }
+  __device__ __forceinline__ int column(int i) const { return block(i) * MOE_BLOCK8; }
+  __device__ __forceinline__ int valid(int i) const { return max(0, min(MOE_BLOCK8, H - column(i))); }
+};
+
+template <class T, class P, bool VEC, int PER>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    rms_fwd_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ res, int64_t ldr,
+                   const P* __restrict__ weight, T* __restrict__ h, T* __restrict__ y, uint8_t* __restrict__ codes,
+                   uint8_t* __restrict__ scales, float* __restrict__ rstd, int N, int H, int nb, int tpr, float eps) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr bool AHEAD = VEC && PER * (int)sizeof(T) <= 8;
+  __shared__ float red[2][kMaxThreads / 32];
+  const RowPlace at(tpr, H);
+  const float inv_h = 1.0f / (float)H;
+  Pack<P, 8> w[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    w[i] = one_pack<P, 8>();
+    if (weight && at.valid(i)) w[i] = load_raw8<P, VEC>(weight + at.column(i), at.lane16, at.valid(i));
+  }
+  Pack<T, 8> nx[PER], nr[PER];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int v = row < N ? at.valid(i) : 0;
+      nx[i] = load_raw8<T, VEC>(x + (v ? row * ldx + at.column(i) : 0), at.lane16, v);
+      if (res) nr[i] = load_raw8<T, VEC>(res + (v ? row * ldr + at.column(i) : 0), at.lane16, v);
+    }
+  };
+  if (AHEAD) load((int64_t)blockIdx.x * at.rows + at.group);
+  int it = 0;
+  for (int64_t base = (int64_t)blockIdx.x * at.rows; base < N; base += (int64_t)gridDim.x * at.rows, ++it) {
+    const int64_t row = base + at.group;
+    if (!AHEAD) load(row);
+    Pack<T, 8> v[PER];
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      float f[8];
+      unpack<T, 8>(nx[i], f);
+      if (res) {
+        float r[8];
+        unpack<T, 8>(nr[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += r[j];
+        v[i] = pack<T, 8>(f);
+        unpack<T, 8>(v[i], f);       // what is kept
+      } else {
+        v[i] = nx[i];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq = fmaf(f[j], f[j], sq);
+    }
+    if (AHEAD) load(row + (int64_t)gridDim.x * at.rows);
+    const float rs = 1.0f / sqrtf(row_sum(sq, tpr, at.group, red[it & 1]) * inv_h + eps);
+    if (row >= N) continue;          // a whole row group, so whole warps; the barrier is behind it
+    if (rstd && at.t == 0) rstd[row] = rs;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int n = at.valid(i);
+      if (h) store_raw8<T, VEC>(h + row * H + at.column(i), at.lane16, n, v[i]);
+      float f[8], g[8];
+      unpack<T, 8>(v[i], f);
+      unpack<P, 8>(w[i], g);
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] = f[j] * rs * g[j];
+        m = fmaxf(m, finite_magnitude(f[j]));
+      }
+      if (y) store_raw8<T, VEC>(y + row * H + at.column(i), at.lane16, n, pack<T, 8>(f));
+      if (codes) {
+        const int byte = block_scale_byte(half_warp_max(m));
+        store_codes8<VEC>(codes + row * H + at.column(i), at.lane16, n, block_codes(f, byte));
+        if (n && at.lane16 == 0) scales[row * nb + at.block(i)] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+// Each thread keeps the sums of dy xh of its columns in registers over all its rows.  The row groups of a block add
+// theirs up in order, into part[block][H]; rms_param_kernel adds the blocks in order.
+template <class T, class P, bool VEC, int PER>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    rms_bwd_kernel(const T* __restrict__ h, int64_t ldh, const P* __restrict__ weight, const float* __restrict__ rstd,
+                   const T* __restrict__ dy, int64_t lddy, const T* __restrict__ dh, int64_t lddh, T* __restrict__ dx,
+                   float* __restrict__ part, int N, int H, int tpr) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr bool AHEAD = VEC && PER * (int)sizeof(T) <= 4;
+  __shared__ float red[2][kMaxThreads / 32];
+  extern __shared__ float cols[];    // [H] where a block holds several rows
+  const RowPlace at(tpr, H);
+  const float inv_h = 1.0f / (float)H;
+  float gw[PER][8];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[i][j] = 0.0f;
+  Pack<T, 8> nh[PER], ng[PER];
+  float rs_next = 0.0f;
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int v = row < N ? at.valid(i) : 0;
+      nh[i] = load_raw8<T, VEC>(h + (v ? row * ldh + at.column(i) : 0), at.lane16, v);
+      ng[i] = load_raw8<T, VEC>(dy + (v ? row * lddy + at.column(i) : 0), at.lane16, v);
+    }
+    rs_next = row < N ? rstd[row] : 0.0f;
+  };
+  auto weights = [&](int i, float (&f)[8]) {
+    if (weight) {
+      const Pack<P, 8> p = load_raw8<P, VEC>(weight + (at.valid(i) ? at.column(i) : 0), at.lane16, at.valid(i));
+      unpack<P, 8>(p, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+    }
+  };
+  if (AHEAD) load((int64_t)blockIdx.x * at.rows + at.group);
+  int it = 0;
+  for (int64_t base = (int64_t)blockIdx.x * at.rows; base < N; base += (int64_t)gridDim.x * at.rows, ++it) {
+    const int64_t row = base + at.group;
+    if (!AHEAD) load(row);
+    Pack<T, 8> v[PER], g[PER], d[PER];
+    const float rs = rs_next;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      v[i] = nh[i];
+      g[i] = ng[i];
+      const int n = row < N && dx && dh ? at.valid(i) : 0;
+      d[i] = load_raw8<T, VEC>(n ? dh + row * lddh + at.column(i) : h, at.lane16, n);
+    }
+    if (AHEAD) load(row + (int64_t)gridDim.x * at.rows);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      float a[8], b[8], w[8];
+      unpack<T, 8>(v[i], a);
+      unpack<T, 8>(g[i], b);
+      weights(i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = a[j] * rs;
+        gw[i][j] = fmaf(b[j], xh, gw[i][j]);
+        sum = fmaf(b[j] * w[j], xh, sum);
+      }
+    }
+    if (!dx) continue;               // all threads alike
+    const float c = row_sum(sum, tpr, at.group, red[it & 1]) * inv_h;
+    if (row >= N) continue;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      float a[8], b[8], w[8], e[8];
+      unpack<T, 8>(v[i], a);
+      unpack<T, 8>(g[i], b);
+      unpack<T, 8>(d[i], e);
+      weights(i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = fmaf(rs, b[j] * w[j] - a[j] * rs * c, e[j]);
+      store_raw8<T, VEC>(dx + row * H + at.column(i), at.lane16, at.valid(i), pack<T, 8>(e));
+    }
+  }
+  if (!part) return;
+  float* out = part + (int64_t)blockIdx.x * H;
+  for (int r = 0; r < at.rows; ++r) {
+    if (r > 0) __syncthreads();
+    if (at.group != r) continue;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = block_column<VEC>(at.lane16, j);
+        if (c < at.valid(i)) {
+          const float s = gw[i][j] + (r > 0 ? cols[at.column(i) + c] : 0.0f);
+          if (r + 1 < at.rows) cols[at.column(i) + c] = s;
+          else out[at.column(i) + c] = s;
+        }
+      }
+  }
+}
+
+// dweight[c] = the sum of part[0 .. groups - 1][c], 32 columns a block: each of 32 warps adds every 32nd, then the 32
+// sums are added in order.
+__global__ void __launch_bounds__(1024) rms_param_kernel(const float* __restrict__ part, float* __restrict__ dweight,
+                                                         int groups, int H) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < H) {
+#pragma unroll 10
+    for (int g = warp; g < groups; g += 32) s += part[(int64_t)g * H + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < H) {
+    for (int g = 1; g < 32; ++g) s += sums[g][lane];
+    dweight[c] = s;
+  }
+}
+
+int rms_validate(const moe_rmsnorm_config* c) {
+  if (!c || c->N < 0 || c->H < 1 || !(c->eps >= 0.0f) || c->eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  return c->H > MOE_RMSNORM_MAX_H ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+// Threads of a row and rows of a block, by the row's blocks of 128 columns: a warp a row up to 1024 columns, then 32
+// values a thread.  Threads with fewer values need fewer registers, and more blocks of them run on a SM.
+struct RmsShape {
+  int nb, per, tpr, rows, most;
+};
+RmsShape rms_shape(int H) {
+  RmsShape s;
+  s.nb = (H + MOE_BLOCK8 - 1) / MOE_BLOCK8;
+  s.per = s.nb <= 2 ? 1 : s.nb <= 4 ? 2 : 4;
+  s.tpr = ((s.nb + s.per - 1) / s.per * 16 + 31) / 32 * 32;
+  s.rows = std::max(1, 256 / s.tpr);
+  s.most = 304 * (4 / s.per);
+  return s;
+}
+int rms_blocks(int N, const RmsShape& s) { return (int)std::min<int64_t>(s.most, ((int64_t)N + s.rows - 1) / s.rows); }
+
+// f(T, P, VEC, PER) with compile-time values.
+template <class F>
+cudaError_t with_rms(int type, int param_type, bool vec, int per, F&& f) {
+  return with_type(type, [&](auto tv) {
+    auto by_param = [&](auto pv) {
+      auto by_per = [&](auto vv) {
+        if (per == 1) return f(tv, pv, vv, std::integral_constant<int, 1>{});
+        if (per == 2) return f(tv, pv, vv, std::integral_constant<int, 2>{});
+        return f(tv, pv, vv, std::integral_constant<int, 4>{});
+      };
+      return vec ? by_per(std::true_type{}) : by_per(std::false_type{});
+    };
+    if (param_type == MOE_TYPE_F32) return by_param(float{});
+    return by_param(tv);
+  });
+}
+
+bool vec_rows(const void* p, int64_t ld, int type) {
+  return !p || (aligned_to(p, 16) && ld * type_size(type) % 16 == 0);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_rmsnorm_workspace_bytes(const moe_rmsnorm_config* cfg, size_t* bwd_bytes) {
+  const int v = rms_validate(cfg);
+  if (v != MOE_OK) return v;
+  if (bwd_bytes) *bwd_bytes = sizeof(WsHeader) + align256((size_t)rms_blocks(cfg->N, rms_shape(cfg->H)) * cfg->H * 4);
+  return MOE_OK;
+}
+
+int moe_rmsnorm_forward(const moe_rmsnorm_config* cfg, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                        const void* weight, void* h, void* y, uint8_t* codes, uint8_t* scales, float* rstd,
+                        int32_t type, int32_t param_type, void* stream) {
+  const int v = rms_validate(cfg);
+  if (v != MOE_OK) return v;
+  const moe_rmsnorm_config& c = *cfg;
+  if (!known_type(type) || !(param_type == type || param_type == MOE_TYPE_F32) || ldx < c.H || (residual && ldr < c.H))
+    return MOE_ERR_INVALID_ARG;
+  const size_t ts = type_size(type);
+  if (!aligned_to(weight, type_size(param_type)) || !aligned_to(rstd, 4) || !aligned_to(residual, ts) ||
+      !aligned_to(h, ts) || !aligned_to(y, ts) || (codes != nullptr) != (scales != nullptr) || (h && !residual))
+    return MOE_ERR_INVALID_ARG;
+  if (c.N == 0) return MOE_OK;
+  if (!x || !aligned_to(x, ts)) return MOE_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const RmsShape r = rms_shape(c.H);
+  const bool vec = c.H % 8 == 0 && vec_rows(x, ldx, type) && vec_rows(residual, ldr, type) && vec_rows(h, c.H, type) &&
+                   vec_rows(y, c.H, type) && aligned_to(weight, 16) && aligned_to(codes, 8);
+  return timed_launch(MOE_K_RMS_FWD, "rms norm", s, [&] {
+    return with_rms(type, param_type, vec, r.per, [&](auto tv, auto pv, auto vv, auto n) {
+      using T = decltype(tv);
+      using P = decltype(pv);
+      return launch_pdl(rms_fwd_kernel<T, P, decltype(vv)::value, decltype(n)::value>, dim3(rms_blocks(c.N, r)),
+                        dim3(r.tpr * r.rows), 0, s, static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr,
+                        static_cast<const P*>(weight), static_cast<T*>(h), static_cast<T*>(y), codes, scales, rstd, c.N,
+                        c.H, r.nb, r.tpr, c.eps);
+    });
+  });
+}
+
+int moe_rmsnorm_backward(const moe_rmsnorm_config* cfg, const void* h, int64_t ldh, const void* weight,
+                         const float* rstd, const void* dy, int64_t lddy, const void* dh, int64_t lddh, void* dx,
+                         float* dweight, int32_t type, int32_t param_type, void* ws, size_t ws_bytes, void* stream) {
+  int v = rms_validate(cfg);
+  if (v != MOE_OK) return v;
+  const moe_rmsnorm_config& c = *cfg;
+  if (!known_type(type) || !(param_type == type || param_type == MOE_TYPE_F32) || ldh < c.H || lddy < c.H ||
+      (dh && lddh < c.H))
+    return MOE_ERR_INVALID_ARG;
+  const size_t ts = type_size(type);
+  if (!aligned_to(weight, type_size(param_type)) || !aligned_to(dweight, 4) || !aligned_to(dh, ts) || !aligned_to(dx, ts))
+    return MOE_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c.N == 0) {
+    if (!dweight) return MOE_OK;
+    const cudaError_t e = cudaMemsetAsync(dweight, 0, (size_t)c.H * 4, s);
+    return e == cudaSuccess ? MOE_OK : record_cuda_error(e, "clear the norm's gradient");
+  }
+  if (!h || !dy || !rstd || !aligned_to(h, ts) || !aligned_to(dy, ts) || !aligned_to(rstd, 4) || !ws || !aligned_to(ws, 16))
+    return MOE_ERR_INVALID_ARG;
+  size_t need = 0;
+  moe_rmsnorm_workspace_bytes(cfg, &need);
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!dx && !dweight) return MOE_OK;
+  const RmsShape r = rms_shape(c.H);
+  const bool vec = c.H % 8 == 0 && vec_rows(h, ldh, type) && vec_rows(dy, lddy, type) && vec_rows(dh, lddh, type) &&
+                   vec_rows(dx, c.H, type) && aligned_to(weight, 16);
+  float* part = dweight ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader)) : nullptr;
+  const int blocks = rms_blocks(c.N, r);
+  v = timed_launch(MOE_K_RMS_BWD, "rms norm backward", s, [&] {
+    return with_rms(type, param_type, vec, r.per, [&](auto tv, auto pv, auto vv, auto n) {
+      using T = decltype(tv);
+      using P = decltype(pv);
+      return launch_pdl(rms_bwd_kernel<T, P, decltype(vv)::value, decltype(n)::value>, dim3(blocks),
+                        dim3(r.tpr * r.rows), r.rows > 1 ? c.H * 4 : 0, s, static_cast<const T*>(h), ldh,
+                        static_cast<const P*>(weight), rstd, static_cast<const T*>(dy), lddy, static_cast<const T*>(dh),
+                        lddh, static_cast<T*>(dx), part, c.N, c.H, r.tpr);
+    });
+  });
+  if (v != MOE_OK || !dweight) return v;
+  return timed_launch(MOE_K_RMS_BWD, "rms norm weight gradient", s, [&] {
+    return launch_pdl(rms_param_kernel, dim3((c.H + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part), dweight,
+                      blocks, c.H);
+  });
+}
+
+}  // extern "C"
