@@ -17,31 +17,33 @@ constexpr int kBatch = 4;   // blocks a half warp has in flight
 // VEC: rows of x and codes lie on 16 and 8 bytes and hold a multiple of eight values.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    pack_rows_kernel(const T* __restrict__ x, int64_t ldx, int64_t blocks, int nb, int H, uint8_t* __restrict__ codes,
+    pack_rows_kernel(const T* __restrict__ x, int64_t ldx, int blocks, FastDiv nb, int H, uint8_t* __restrict__ codes,
                      uint8_t* __restrict__ scales) {
   pdl_wait();
   pdl_trigger();
   const int lane16 = threadIdx.x & 15;
   const int64_t first = ((int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kBatch;
-  float v[kBatch][8];
-  int64_t row[kBatch];
-  int b[kBatch], valid[kBatch];
+  f32x2 f[kBatch][4];
+  int64_t to[kBatch];
+  int valid[kBatch];
+  Pack<T, 8> raw[kBatch];
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
-    const int64_t at = first + j;
-    row[j] = at / nb;
-    b[j] = (int)(at - row[j] * nb);
-    valid[j] = at < blocks ? min(MOE_BLOCK8, H - b[j] * MOE_BLOCK8) : 0;
-    load_block8<T, VEC>(x + (valid[j] ? row[j] * ldx + b[j] * MOE_BLOCK8 : 0), lane16, valid[j], v[j]);
+    const int at = (int)min(first + j, (int64_t)blocks - 1);
+    const int row = (int)nb(at), col = (at - row * (int)nb.d) * MOE_BLOCK8;
+    valid[j] = first + j < blocks ? min(MOE_BLOCK8, H - col) : 0;
+    to[j] = (int64_t)row * H + col;
+    raw[j] = load_block8<T, VEC>(x + row * ldx + col, lane16, valid[j]);
   }
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
-    float m = 0.0f;
+  for (int j = 0; j < kBatch; ++j) unpack2<T, 8>(raw[j], f[j]);
+  float m[kBatch];
+  const bool infinite = blocks_max<kBatch>(f, m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_magnitude(v[j][i]));
-    const int byte = block_scale_byte(half_warp_max(m));
+  for (int j = 0; j < kBatch; ++j) {
+    const int byte = block_scale_byte(m[j]);
     if (valid[j]) {
-      store_codes8<VEC>(codes + row[j] * H + b[j] * MOE_BLOCK8, lane16, valid[j], block_codes(v[j], byte));
+      store_codes8<VEC>(codes + to[j], lane16, valid[j], block_codes(f[j], byte, infinite));
       if (lane16 == 0) scales[first + j] = (uint8_t)byte;
     }
   }
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    unpack_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t blocks, int nb,
+    unpack_rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int blocks, FastDiv nb,
                        int H, T* __restrict__ y) {
   pdl_wait();
   pdl_trigger();
@@ -60,12 +62,12 @@ __global__ void __launch_bounds__(kThreads)
   int64_t from[kBatch];
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
-    const int64_t at = first + j, row = at / nb;
-    const int b = (int)(at - row * nb);
-    valid[j] = at < blocks ? min(MOE_BLOCK8, H - b * MOE_BLOCK8) : 0;
-    from[j] = row * H + b * MOE_BLOCK8;
+    const int at = (int)min(first + j, (int64_t)blocks - 1);
+    const int row = (int)nb(at), col = (at - row * (int)nb.d) * MOE_BLOCK8;
+    valid[j] = first + j < blocks ? min(MOE_BLOCK8, H - col) : 0;
+    from[j] = (int64_t)row * H + col;
     c[j] = 0;
-    byte[j] = valid[j] ? scales[at] : 127;
+    byte[j] = scales[at];
     if constexpr (VEC) {
       if (lane16 * 8 < valid[j]) c[j] = *reinterpret_cast<const uint64_t*>(codes + from[j] + lane16 * 8);
     } else {
@@ -76,15 +78,14 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
-    const float s = block_scale(byte[j]);
-    float v[8];
+    const f32x2 s(block_scale(byte[j]));
+    f32x2 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = e4m3_values((uint32_t)(c[j] >> (16 * i)) & 0xFFFFu);
-      v[2 * i] = f.x * s;
-      v[2 * i + 1] = f.y * s;
+      const float2 p = e4m3_values((uint32_t)(c[j] >> (16 * i)) & 0xFFFFu);
+      v[i] = mul2(f32x2(p.x, p.y), s);
     }
-    store_block8<T, VEC>(y + (valid[j] ? from[j] : 0), lane16, valid[j], v);
+    store_block8<T, VEC>(y + from[j], lane16, valid[j], pack2<T, 8>(v));
   }
 }
 
@@ -94,43 +95,58 @@ __global__ void __launch_bounds__(kThreads)
     pack_weight_kernel(const T* __restrict__ w, int O, int K, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float most[kThreads / 32];
+  __shared__ float most[2][kThreads / 32];
   const int nk = (K + MOE_BLOCK8 - 1) / MOE_BLOCK8, no = (O + MOE_BLOCK8 - 1) / MOE_BLOCK8;
   const int kb = blockIdx.x % nk;
-  const int64_t eo = blockIdx.x / nk;               // (expert, block of rows)
-  const int ob = (int)(eo % no);
+  const int eo = blockIdx.x / nk;                   // (expert, block of rows)
+  const int ob = eo % no;
   const int64_t e = eo / no;
   const int lane16 = threadIdx.x & 15, sub = threadIdx.x >> 4;
   const int valid = min(MOE_BLOCK8, K - kb * MOE_BLOCK8);
   const int64_t base = (e * O + ob * MOE_BLOCK8) * K + kb * MOE_BLOCK8;
   const int rows = min(MOE_BLOCK8, O - ob * MOE_BLOCK8);
-  float v[8][8], m = 0.0f;
+  f32x2 f[8][4];
+  Pack<T, 8> raw[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int r = sub + 16 * j;
-    load_block8<T, VEC>(w + base + (r < rows ? (int64_t)r * K : 0), lane16, r < rows ? valid : 0, v[j]);
+    raw[j] = load_block8<T, VEC>(w + base + (r < rows ? (int64_t)r * K : 0), lane16, r < rows ? valid : 0);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 8; ++j) unpack2<T, 8>(raw[j], f[j]);
+  auto among_threads = [&](float m, int turn) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_magnitude(v[j][i]));
-  m = half_warp_max(m);
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-  if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
-  __syncthreads();
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if ((threadIdx.x & 31) == 0) most[turn][threadIdx.x >> 5] = m;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, most[i]);
+    for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, most[turn][i]);
+    return m;
+  };
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, lane_max(f[j]));
+  m = among_threads(m, 0);
+  const bool infinite = m == INFINITY;              // of all threads alike
+  if (infinite) {
+    m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, lane_finite_max(f[j]));
+    m = among_threads(m, 1);
+  }
   const int byte = block_scale_byte(m);
   if (threadIdx.x == 0) scales[blockIdx.x] = (uint8_t)byte;   // [e][ob][kb]
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int r = sub + 16 * j;
-    if (r < rows) store_codes8<VEC>(codes + base + (int64_t)r * K, lane16, valid, block_codes(v[j], byte));
+    if (r < rows) store_codes8<VEC>(codes + base + (int64_t)r * K, lane16, valid, block_codes(f[j], byte, infinite));
   }
 }
 
 constexpr int kMaxWidth = 1 << 20;
 inline int64_t row_blocks(int64_t N, int nb) { return (N * nb + kThreads / 16 * kBatch - 1) / (kThreads / 16 * kBatch); }
+// Blocks of 128 are counted in 31 bits (2.7e11 values).
+inline bool too_many(int64_t N, int64_t nb) { return N > INT32_MAX / nb; }
 
 }  // namespace
 
@@ -142,7 +158,7 @@ cudaError_t launch_pack_rows(const void* x, int64_t ldx, int type, int64_t N, in
     using T = decltype(tv);
     auto go = [&](auto kern) {
       return launch_pdl(kern, dim3((unsigned)row_blocks(N, nb)), dim3(kThreads), 0, s, static_cast<const T*>(x), ldx,
-                        N * nb, nb, H, codes, scales);
+                        (int)(N * nb), FastDiv(nb), H, codes, scales);
     };
     return vec ? go(pack_rows_kernel<T, true>) : go(pack_rows_kernel<T, false>);
   });
@@ -155,8 +171,8 @@ cudaError_t launch_unpack_rows(const uint8_t* codes, const uint8_t* scales, int6
   return with_type(type, [&](auto tv) {
     using T = decltype(tv);
     auto go = [&](auto kern) {
-      return launch_pdl(kern, dim3((unsigned)row_blocks(N, nb)), dim3(kThreads), 0, s, codes, scales, N * nb, nb, H,
-                        static_cast<T*>(y));
+      return launch_pdl(kern, dim3((unsigned)row_blocks(N, nb)), dim3(kThreads), 0, s, codes, scales, (int)(N * nb),
+                        FastDiv(nb), H, static_cast<T*>(y));
     };
     return vec ? go(unpack_rows_kernel<T, true>) : go(unpack_rows_kernel<T, false>);
   });
@@ -172,7 +188,7 @@ int moe_blocks8_pack(const void* x, int64_t ldx, int32_t type, int64_t N, int32_
                      void* stream) {
   if (N < 0 || H < 1 || !known_type(type) || ldx < H) return MOE_ERR_INVALID_ARG;
   const int64_t nb = (H + MOE_BLOCK8 - 1) / MOE_BLOCK8;
-  if (H > kMaxWidth || N > (int64_t)INT32_MAX * (kThreads / 16) / nb) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H > kMaxWidth || too_many(N, nb)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (N == 0) return MOE_OK;
   if (!x || !codes || !scales || !aligned_to(x, type_size(type))) return MOE_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -184,7 +200,7 @@ int moe_blocks8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t N, i
                        void* stream) {
   if (N < 0 || H < 1 || !known_type(type)) return MOE_ERR_INVALID_ARG;
   const int64_t nb = (H + MOE_BLOCK8 - 1) / MOE_BLOCK8;
-  if (H > kMaxWidth || N > (int64_t)INT32_MAX * (kThreads / 16) / nb) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H > kMaxWidth || too_many(N, nb)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (N == 0) return MOE_OK;
   if (!y || !codes || !scales || !aligned_to(y, type_size(type))) return MOE_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -26,12 +26,7 @@ __device__ __forceinline__ float finite_magnitude(float v) {
   const float a = fabsf(v);
   return a < INFINITY ? a : 0.0f;
 }
-// v / scale, ready for e4m3: what is not finite becomes NaN.
-__device__ __forceinline__ float block_quotient(float v, float inverse, float limit) {
-  const float q = v * inverse;
-  return fabsf(v) < INFINITY ? fminf(fmaxf(q, -limit), limit) : __uint_as_float(0x7FFFFFFFu);
-}
-// Two values to two e4m3 codes (lo in the low byte), to nearest even.
+// Two values to two e4m3 codes (lo in the low byte), to nearest even; NaN to NaN.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -44,50 +39,32 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t pair) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// Eight values of a block by one lane, after amax is known: eight codes.
-__device__ __forceinline__ uint2 block_codes(const float (&v)[8], int byte) {
-  const float inv = block_scale_inverse(byte), lim = block_code_limit(byte);
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = block_quotient(v[i], inv, lim);
-  return make_uint2(e4m3_pair(q[0], q[1]) | e4m3_pair(q[2], q[3]) << 16, e4m3_pair(q[4], q[5]) | e4m3_pair(q[6], q[7]) << 16);
-}
-// The largest over the 16 lanes of a half warp.
-__device__ __forceinline__ float half_warp_max(float v) {
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
-
-// A half warp's lane holds eight of the 128 values of a block: consecutive ones where the row lies on 16 bytes (VEC),
-// else every sixteenth.  f(i, column in block).
+// A half warp's lane holds eight of the 128 values of a block, as four pairs: consecutive ones where the row lies on 16
+// bytes (VEC), else every sixteenth.
 template <bool VEC>
 __device__ __forceinline__ int block_column(int lane16, int i) { return VEC ? lane16 * 8 + i : lane16 + 16 * i; }
 
-// Loads a lane's eight of the block that starts at p, `valid` values long; zeros past them.
+// The lane's eight of the block that starts at p, `valid` values long (a multiple of eight with VEC); zeros past them.
 template <class T, bool VEC>
-__device__ __forceinline__ void load_block8(const T* p, int lane16, int valid, float (&v)[8]) {
-  if constexpr (VEC) {   // valid is a multiple of 8 here
-    if (lane16 * 8 < valid) {
-      const Pack<T, 8> a = load_pack<T, 8>(p + lane16 * 8);
-      unpack<T, 8>(a, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = lane16 + 16 * i < valid ? to_f32<T>(p[lane16 + 16 * i]) : 0.0f;
-  }
-}
-template <class T, bool VEC>
-__device__ __forceinline__ void store_block8(T* p, int lane16, int valid, const float (&v)[8]) {
+__device__ __forceinline__ Pack<T, 8> load_block8(const T* p, int lane16, int valid) {
+  Pack<T, 8> a = zero_pack<T, 8>();
   if constexpr (VEC) {
-    if (lane16 * 8 < valid) store_pack<T, 8>(p + lane16 * 8, pack<T, 8>(v));
+    if (lane16 * 8 < valid) a = load_pack<T, 8>(p + lane16 * 8);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (lane16 + 16 * i < valid) p[lane16 + 16 * i] = from_f32<T>(v[i]);
+      if (lane16 + 16 * i < valid) a.v[i] = p[lane16 + 16 * i];
+  }
+  return a;
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void store_block8(T* p, int lane16, int valid, const Pack<T, 8>& a) {
+  if constexpr (VEC) {
+    if (lane16 * 8 < valid) store_pack<T, 8>(p + lane16 * 8, a);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane16 + 16 * i < valid) p[lane16 + 16 * i] = a.v[i];
   }
 }
 template <bool VEC>
@@ -101,5 +78,79 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int lane16, int valid, 
       if (lane16 + 16 * i < valid) p[lane16 + 16 * i] = (uint8_t)(all >> (8 * i));
   }
 }
+
+// The largest magnitude among a lane's eight (infinity where there is one, NaN passed over), and the largest finite one.
+__device__ __forceinline__ float lane_max(const f32x2 (&f)[4]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f[i].get(a, b);
+    m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+  }
+  return m;
+}
+__device__ __forceinline__ float lane_finite_max(const f32x2 (&f)[4]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f[i].get(a, b);
+    m = fmaxf(m, fmaxf(finite_magnitude(a), finite_magnitude(b)));
+  }
+  return m;
+}
+// The largest finite magnitude of each of PER blocks that a half warp holds; the whole warp calls it.  Infinities, which
+// are rare, cost a second search; returns whether there was one among the warp's.
+template <int PER>
+__device__ __forceinline__ bool blocks_max(const f32x2 (&f)[PER][4], float (&m)[PER]) {
+  auto among_lanes = [&] {   // the blocks' shuffles side by side
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+  };
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    m[i] = lane_max(f[i]);
+    most = fmaxf(most, m[i]);
+  }
+  among_lanes();
+  if (!__any_sync(0xffffffffu, most == INFINITY)) return false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) m[i] = lane_finite_max(f[i]);
+  among_lanes();
+  return true;
+}
+// A lane's eight codes.  infinite: there may be infinities (else the quotients are within the codes, but for byte 247).
+__device__ __forceinline__ uint2 block_codes(const f32x2 (&f)[4], int byte, bool infinite) {
+  const float inv = block_scale_inverse(byte);
+  const f32x2 inv2(inv);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    mul2(f[i], inv2).get(a, b);
+    if (infinite || byte >= 247) {
+      const float lim = block_code_limit(byte);
+      a = fabsf(a) < INFINITY ? fminf(fmaxf(a, -lim), lim) : __uint_as_float(0x7FFFFFFFu);
+      b = fabsf(b) < INFINITY ? fminf(fmaxf(b, -lim), lim) : __uint_as_float(0x7FFFFFFFu);
+    }
+    c[i] = e4m3_pair(a, b);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// n / d for n < 2^31, by a multiplication: m = floor(2^32 (2^s - d) / d) + 1 with 2^s >= d (Granlund and Montgomery,
+// "Division by invariant integers using multiplication", 1994).
+struct FastDiv {
+  uint32_t d, m, s;
+  explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
 
 }  // namespace moe

@@ -132,6 +132,12 @@ __device__ __forceinline__ LinTile lin_tile(const LinGemm& p, const int* offs, c
   return t;
 }
 
+// One lane of the (whole) warp: true there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
 __device__ __forceinline__ void tc_mma_pair_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
   int* first = offs + p.E + 1;
   int* most = reinterpret_cast<int*>(tmem_slot + 2);   // rows of the expert that has most
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known to be uniform
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
@@ -357,7 +363,11 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs (even CTA)
+    // The whole warp walks the loop, so that descriptors and addresses are computed once for all lanes in uniform
+    // registers; one elected lane issues.  (Computed by a single lane of a divergent branch they cost a K block of e4m3
+    // 985 cycles without any load to wait for, where its MMAs need 512.)
     if (leader) {
+      const bool one = elect_one();
       int stage = 0, it = 0, slot = 0;
       uint32_t phase = 0, sphase = 0, group = 0;   // group: scales copied so far
       bool ok = true;
@@ -367,34 +377,34 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
         // one accumulator after the other (an empty share still passes its accumulator on)
         for (int k0 = t.kb0; ok && (k0 < t.kb1 || k0 == t.kb0); k0 += step, ++it) {
           const int acc = it & 1;
-          int good = 1;
-          if (lane == 0) {
-            if constexpr (MX) {   // the columns that the last accumulator shares with this one
-              if (it > 0) good = wait_bounded(tempty_bar(0), (it - 1) & 1, abort_flag, p.limit_ns, p.status, 802);
-            } else {
-              good = wait_bounded(tempty_bar(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.limit_ns, p.status, 802);
-            }
+          bool good = true;
+          if constexpr (MX) {   // the columns that the last accumulator shares with this one
+            if (it > 0) good = wait_bounded(tempty_bar(0), (it - 1) & 1, abort_flag, p.limit_ns, p.status, 802);
+          } else {
+            good = wait_bounded(tempty_bar(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.limit_ns, p.status, 802);
           }
-          if (!__shfl_sync(0xffffffffu, good, 0)) {
+          if (!__all_sync(0xffffffffu, good)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t tacc = tmem_base + acc * (MX ? S::TM_ACC1 : 256);
           for (int kb = k0; kb < min(t.kb1, k0 + step); ++kb) {
-            if (lane == 0) good = wait_bounded(full_bar(stage), phase, abort_flag, p.limit_ns, p.status, 803);
-            if (MX && good && (kb & 3) == 0 && lane == 0)
-              good = wait_bounded(sfull_bar(slot), sphase, abort_flag, p.limit_ns, p.status, 804);
-            if (!__shfl_sync(0xffffffffu, good, 0)) {
+            good = wait_bounded(full_bar(stage), phase, abort_flag, p.limit_ns, p.status, 803);
+            if (MX && (kb & 3) == 0)
+              good = good && wait_bounded(sfull_bar(slot), sphase, abort_flag, p.limit_ns, p.status, 804);
+            if (!__all_sync(0xffffffffu, good)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint32_t sa = sbase + stage * S::STAGE, sb = sa + S::HALF;
-            if (lane == 0) {
-              if constexpr (MX) {
-                // two sets of scale columns in turn: four of A and eight of B
-                const uint32_t sfa = tmem_base + S::TM_SF + 16 * (group & 1), sfb = sfa + 8;
+            if constexpr (MX) {
+              // two sets of scale columns in turn: four of A and eight of B
+              const uint32_t sfa = tmem_base + S::TM_SF + 16 * (group & 1), sfb = sfa + 8;
+              const uint32_t idesc = instr_desc_mx(256, 256, B_MN) | (uint32_t)(kb & 3) << 4 | (uint32_t)(kb & 3) << 29;
+              const uint64_t ad = smem_desc_sw128(sa, 0, 1024), bd = smem_desc_sw128(sb, B_MN ? 16384 : 0, 1024);
+              if (one) {
                 if ((kb & 3) == 0) {
                   const uint32_t from = sbase + S::SF + slot * S::SF_BYTES;
                   tc_copy_scales_pair(sfa, from);
@@ -402,24 +412,22 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
                   tc_copy_scales_pair(sfb + 4, from + 1024);
                   tc_commit_pair(sempty_bar(slot), 0x3);
                 }
-                const uint32_t idesc = instr_desc_mx(256, 256, B_MN) | (uint32_t)(kb & 3) << 4 | (uint32_t)(kb & 3) << 29;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint64_t ad = smem_desc_sw128(sa + kk * 32, 0, 1024);
-                  const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 4096, 16384, 1024) : smem_desc_sw128(sb + kk * 32, 0, 1024);
-                  tc_mma_pair_mx(tacc, ad, bd, idesc, sfa, sfb, kb != k0 || kk != 0 ? 1u : 0u);
-                }
-              } else {
-                constexpr uint32_t idesc = instr_desc_bf16(256, 256, A_MN, B_MN);
-                const int steps = MODE == LIN_DW ? min(4, (t.rows - kb * 64 + 15) >> 4) : 4;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint64_t ad = A_MN ? smem_desc_sw128(sa + kk * 2048, 8192, 1024) : smem_desc_sw128(sa + kk * 32, 0, 1024);
-                  const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 0, 1024);
-                  if (kk < steps) tc_mma_pair(tacc, ad, bd, idesc, kb != k0 || kk != 0 ? 1u : 0u);
-                }
+                for (int kk = 0; kk < 4; ++kk)   // 32 bytes of K on, in units of 16; across it, 32 rows of 128 bytes
+                  tc_mma_pair_mx(tacc, ad + 2 * kk, bd + (B_MN ? 256 : 2) * kk, idesc, sfa, sfb, kb != k0 || kk != 0 ? 1u : 0u);
+                tc_commit_pair(empty_bar(stage), 0x3);
               }
-              tc_commit_pair(empty_bar(stage), 0x3);
+            } else {
+              constexpr uint32_t idesc = instr_desc_bf16(256, 256, A_MN, B_MN);
+              const int steps = MODE == LIN_DW ? min(4, (t.rows - kb * 64 + 15) >> 4) : 4;
+              const uint64_t ad = smem_desc_sw128(sa, A_MN ? 8192 : 0, 1024), bd = smem_desc_sw128(sb, B_MN ? 8192 : 0, 1024);
+              if (one) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)   // 16 of K on: 32 bytes, or 16 rows of 128
+                  if (kk < steps)
+                    tc_mma_pair(tacc, ad + (A_MN ? 128 : 2) * kk, bd + (B_MN ? 128 : 2) * kk, idesc, kb != k0 || kk != 0 ? 1u : 0u);
+                tc_commit_pair(empty_bar(stage), 0x3);
+              }
             }
             __syncwarp();
             if (MX && (kb & 3) == 0 && ++slot == S::SF_SLOTS) { slot = 0; sphase ^= 1u; }
@@ -427,11 +435,11 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
             if (++stage == S::STAGES) { stage = 0; phase ^= 1u; }
           }
           if (!ok) break;
-          if (lane == 0) tc_commit_pair(tfull_bar(acc), 0x3);
+          if (one) tc_commit_pair(tfull_bar(acc), 0x3);
           __syncwarp();
         }
       }
-      if (lane == 0) {                              // every MMA has completed before the tensor memory is freed
+      if (one) {                                    // every MMA has completed before the tensor memory is freed
         tc_commit_pair(drain_bar, 0x1);
         volatile int no_abort = 0;
         wait_bounded(drain_bar, 0, &no_abort, max(p.limit_ns, kSettleNs), nullptr, 0);

@@ -14,42 +14,28 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxThreads = 512;
+// Two blocks of 448 threads of the forward share a SM; rows wider than 7168 take one block of up to 512.
+constexpr int rms_threads(int per) { return per <= 2 ? 448 : 512; }
+constexpr int rms_resident(int per) { return per <= 2 ? 2 : 1; }
+constexpr int kMaxRows = 8;
 
-// The sum over a row's threads (tpr of them, whole warps of row group `group`), in a fixed order, in every thread.  red
-// is taken in turn, so that one barrier a row suffices.
-__device__ __forceinline__ float row_sum(float v, int tpr, int group, float* red) {
+// A row's warps leave their sums here, in turn, so that one barrier a row suffices; places without a warp hold 0.
+struct RowSums {
+  float4 v[2][kMaxRows][4];
+};
+__device__ __forceinline__ void clear(RowSums& r) {
+  float4* p = &r.v[0][0][0];
+  for (int i = threadIdx.x; i < 2 * kMaxRows * 4; i += blockDim.x) p[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __syncthreads();
+}
+// The sum over a row's threads (tpr of them, whole warps of row group `group`), in a fixed order, in every thread.
+__device__ __forceinline__ float row_sum(float v, int tpr, int group, int t, float4 (&r)[kMaxRows][4]) {
   v = warp_sum(v);
   if (tpr == 32) return v;
-  const int warps = tpr >> 5, first = group * warps;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((t & 31) == 0) reinterpret_cast<float*>(r[group])[t >> 5] = v;
   __syncthreads();
-  v = 0.0f;
-  for (int i = 0; i < warps; ++i) v += red[first + i];
-  return v;
-}
-
-template <class T, bool VEC>
-__device__ __forceinline__ Pack<T, 8> load_raw8(const T* p, int lane16, int valid) {
-  Pack<T, 8> a = zero_pack<T, 8>();
-  if constexpr (VEC) {
-    if (lane16 * 8 < valid) a = load_pack<T, 8>(p + lane16 * 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane16 + 16 * i < valid) a.v[i] = p[lane16 + 16 * i];
-  }
-  return a;
-}
-template <class T, bool VEC>
-__device__ __forceinline__ void store_raw8(T* p, int lane16, int valid, const Pack<T, 8>& a) {
-  if constexpr (VEC) {
-    if (lane16 * 8 < valid) store_pack<T, 8>(p + lane16 * 8, a);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane16 + 16 * i < valid) p[lane16 + 16 * i] = a.v[i];
-  }
+  const float4 a = r[group][0], b = r[group][1], c = r[group][2], d = r[group][3];
+  return (((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w))) + (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
 }
 
 // A thread's place in its row: block i of its half warp starts at column(i) and has valid(i) columns.
@@ -65,124 +51,123 @@ struct RowPlace {
   }
   __device__ __forceinline__ int block(int i) const { return hw + i * hws; }
   __device__ __forceinline__ int column(int i) const { return block(i) * MOE_BLOCK8; }
+  __device__ __forceinline__ int step() const { return hws * MOE_BLOCK8; }
   __device__ __forceinline__ int valid(int i) const { return max(0, min(MOE_BLOCK8, H - column(i))); }
 };
 
 template <class T, class P, bool VEC, int PER>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+__global__ void __launch_bounds__(rms_threads(PER), rms_resident(PER))
     rms_fwd_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ res, int64_t ldr,
                    const P* __restrict__ weight, T* __restrict__ h, T* __restrict__ y, uint8_t* __restrict__ codes,
                    uint8_t* __restrict__ scales, float* __restrict__ rstd, int N, int H, int nb, int tpr, float eps) {
   pdl_wait();
   pdl_trigger();
-  constexpr bool AHEAD = VEC && PER * (int)sizeof(T) <= 8;
-  __shared__ float red[2][kMaxThreads / 32];
+  __shared__ RowSums sums;
   const RowPlace at(tpr, H);
-  const float inv_h = 1.0f / (float)H;
-  Pack<P, 8> w[PER];
+  const int64_t row = (int64_t)blockIdx.x * at.rows + at.group;
+  const bool there = row < N;        // of a row group, so of whole warps
+  Pack<T, 8> v[PER];
+  const T* xr = x + (there ? row * ldx : 0) + at.column(0);
+  const T* rr = res + (there ? row * ldr : 0) + at.column(0);
+  f32x2 sq(0.0f);
+  {
+    Pack<T, 8> r[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int n = there ? at.valid(i) : 0;
+      v[i] = load_block8<T, VEC>(xr + i * at.step(), at.lane16, n);
+      if (res) r[i] = load_block8<T, VEC>(rr + i * at.step(), at.lane16, n);
+    }
+    if (tpr > 32) clear(sums);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      f32x2 f[4];
+      unpack2<T, 8>(v[i], f);
+      if (res) {
+        f32x2 g[4];
+        unpack2<T, 8>(r[i], g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
+        v[i] = pack2<T, 8>(f);
+        unpack2<T, 8>(v[i], f);      // what is kept
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sq = fma2(f[j], f[j], sq);
+    }
+  }
+  const float rs = 1.0f / sqrtf(row_sum(sq.sum(), tpr, at.group, at.t, sums.v[0]) * (1.0f / (float)H) + eps);
+  if (!there) return;
+  if (rstd && at.t == 0) rstd[row] = rs;
+  const int64_t to = row * H + at.column(0);
+  const f32x2 rs2(rs);
+  f32x2 f[PER][4];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    w[i] = one_pack<P, 8>();
-    if (weight && at.valid(i)) w[i] = load_raw8<P, VEC>(weight + at.column(i), at.lane16, at.valid(i));
+    const int n = at.valid(i);
+    if (h) store_block8<T, VEC>(h + to + i * at.step(), at.lane16, n, v[i]);
+    f32x2 g[4];
+    Pack<P, 8> w = one_pack<P, 8>();
+    if (weight && n) w = load_block8<P, VEC>(weight + at.column(i), at.lane16, n);
+    unpack2<T, 8>(v[i], f[i]);
+    unpack2<P, 8>(w, g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], rs2), g[j]);
+    if (y) store_block8<T, VEC>(y + to + i * at.step(), at.lane16, n, pack2<T, 8>(f[i]));
   }
-  Pack<T, 8> nx[PER], nr[PER];
-  auto load = [&](int64_t row) {
+  if (!codes) return;
+  float m[PER];
+  const bool infinite = blocks_max<PER>(f, m);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int v = row < N ? at.valid(i) : 0;
-      nx[i] = load_raw8<T, VEC>(x + (v ? row * ldx + at.column(i) : 0), at.lane16, v);
-      if (res) nr[i] = load_raw8<T, VEC>(res + (v ? row * ldr + at.column(i) : 0), at.lane16, v);
-    }
-  };
-  if (AHEAD) load((int64_t)blockIdx.x * at.rows + at.group);
-  int it = 0;
-  for (int64_t base = (int64_t)blockIdx.x * at.rows; base < N; base += (int64_t)gridDim.x * at.rows, ++it) {
-    const int64_t row = base + at.group;
-    if (!AHEAD) load(row);
-    Pack<T, 8> v[PER];
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      float f[8];
-      unpack<T, 8>(nx[i], f);
-      if (res) {
-        float r[8];
-        unpack<T, 8>(nr[i], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += r[j];
-        v[i] = pack<T, 8>(f);
-        unpack<T, 8>(v[i], f);       // what is kept
-      } else {
-        v[i] = nx[i];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(f[j], f[j], sq);
-    }
-    if (AHEAD) load(row + (int64_t)gridDim.x * at.rows);
-    const float rs = 1.0f / sqrtf(row_sum(sq, tpr, at.group, red[it & 1]) * inv_h + eps);
-    if (row >= N) continue;          // a whole row group, so whole warps; the barrier is behind it
-    if (rstd && at.t == 0) rstd[row] = rs;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int n = at.valid(i);
-      if (h) store_raw8<T, VEC>(h + row * H + at.column(i), at.lane16, n, v[i]);
-      float f[8], g[8];
-      unpack<T, 8>(v[i], f);
-      unpack<P, 8>(w[i], g);
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] = f[j] * rs * g[j];
-        m = fmaxf(m, finite_magnitude(f[j]));
-      }
-      if (y) store_raw8<T, VEC>(y + row * H + at.column(i), at.lane16, n, pack<T, 8>(f));
-      if (codes) {
-        const int byte = block_scale_byte(half_warp_max(m));
-        store_codes8<VEC>(codes + row * H + at.column(i), at.lane16, n, block_codes(f, byte));
-        if (n && at.lane16 == 0) scales[row * nb + at.block(i)] = (uint8_t)byte;
-      }
-    }
+  for (int i = 0; i < PER; ++i) {
+    const int byte = block_scale_byte(m[i]);
+    store_codes8<VEC>(codes + to + i * at.step(), at.lane16, at.valid(i), block_codes(f[i], byte, infinite));
+    if (at.valid(i) && at.lane16 == 0) scales[row * nb + at.block(i)] = (uint8_t)byte;
   }
 }
 
 // Each thread keeps the sums of dy xh of its columns in registers over all its rows.  The row groups of a block add
 // theirs up in order, into part[block][H]; rms_param_kernel adds the blocks in order.
 template <class T, class P, bool VEC, int PER>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+__global__ void __launch_bounds__(rms_threads(PER), 1)
     rms_bwd_kernel(const T* __restrict__ h, int64_t ldh, const P* __restrict__ weight, const float* __restrict__ rstd,
                    const T* __restrict__ dy, int64_t lddy, const T* __restrict__ dh, int64_t lddh, T* __restrict__ dx,
                    float* __restrict__ part, int N, int H, int tpr) {
   pdl_wait();
   pdl_trigger();
   constexpr bool AHEAD = VEC && PER * (int)sizeof(T) <= 4;
-  __shared__ float red[2][kMaxThreads / 32];
+  constexpr bool LATE = PER * (int)sizeof(T) > 8;   // dh is loaded when it is needed
+  __shared__ RowSums sums;
   extern __shared__ float cols[];    // [H] where a block holds several rows
+  if (tpr > 32) clear(sums);
   const RowPlace at(tpr, H);
   const float inv_h = 1.0f / (float)H;
-  float gw[PER][8];
+  f32x2 gw[PER][4];
 #pragma unroll
   for (int i = 0; i < PER; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) gw[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) gw[i][j] = f32x2(0.0f);
   Pack<T, 8> nh[PER], ng[PER];
   float rs_next = 0.0f;
   auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int v = row < N ? at.valid(i) : 0;
-      nh[i] = load_raw8<T, VEC>(h + (v ? row * ldh + at.column(i) : 0), at.lane16, v);
-      ng[i] = load_raw8<T, VEC>(dy + (v ? row * lddy + at.column(i) : 0), at.lane16, v);
+      nh[i] = load_block8<T, VEC>(h + (v ? row * ldh + at.column(i) : 0), at.lane16, v);
+      ng[i] = load_block8<T, VEC>(dy + (v ? row * lddy + at.column(i) : 0), at.lane16, v);
     }
     rs_next = row < N ? rstd[row] : 0.0f;
   };
-  auto weights = [&](int i, float (&f)[8]) {
-    if (weight) {
-      const Pack<P, 8> p = load_raw8<P, VEC>(weight + (at.valid(i) ? at.column(i) : 0), at.lane16, at.valid(i));
-      unpack<P, 8>(p, f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 1.0f;
-    }
+  auto load_dh = [&](int64_t row, int i) {
+    const int n = row < N && dx && dh ? at.valid(i) : 0;
+    return load_block8<T, VEC>(n ? dh + row * lddh + at.column(i) : h, at.lane16, n);
+  };
+  // Read again for each use, from L1: held, the weights of a row would take the registers of the next row.
+  auto weights = [&](int i, f32x2 (&f)[4]) {
+    const P* p = weight;
+    asm volatile("" : "+l"(p));
+    Pack<P, 8> raw = one_pack<P, 8>();
+    if (p && at.valid(i)) raw = load_block8<P, VEC>(p + at.column(i), at.lane16, at.valid(i));
+    unpack2<P, 8>(raw, f);
   };
   if (AHEAD) load((int64_t)blockIdx.x * at.rows + at.group);
   int it = 0;
@@ -191,41 +176,43 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     if (!AHEAD) load(row);
     Pack<T, 8> v[PER], g[PER], d[PER];
     const float rs = rs_next;
-    float sum = 0.0f;
+    const f32x2 rs2(rs);
+    f32x2 sum(0.0f);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       v[i] = nh[i];
       g[i] = ng[i];
-      const int n = row < N && dx && dh ? at.valid(i) : 0;
-      d[i] = load_raw8<T, VEC>(n ? dh + row * lddh + at.column(i) : h, at.lane16, n);
+      if (!LATE) d[i] = load_dh(row, i);
     }
     if (AHEAD) load(row + (int64_t)gridDim.x * at.rows);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      float a[8], b[8], w[8];
-      unpack<T, 8>(v[i], a);
-      unpack<T, 8>(g[i], b);
+      f32x2 a[4], b[4], w[4];
+      unpack2<T, 8>(v[i], a);
+      unpack2<T, 8>(g[i], b);
       weights(i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = a[j] * rs;
-        gw[i][j] = fmaf(b[j], xh, gw[i][j]);
-        sum = fmaf(b[j] * w[j], xh, sum);
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 xh = mul2(a[j], rs2);
+        gw[i][j] = fma2(b[j], xh, gw[i][j]);
+        sum = fma2(mul2(b[j], w[j]), xh, sum);
       }
     }
     if (!dx) continue;               // all threads alike
-    const float c = row_sum(sum, tpr, at.group, red[it & 1]) * inv_h;
+    const float c = row_sum(sum.sum(), tpr, at.group, at.t, sums.v[it & 1]) * inv_h;
     if (row >= N) continue;
+    const f32x2 by_h(-rs * rs * c);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      float a[8], b[8], w[8], e[8];
-      unpack<T, 8>(v[i], a);
-      unpack<T, 8>(g[i], b);
-      unpack<T, 8>(d[i], e);
+      if (LATE) d[i] = load_dh(row, i);
+      f32x2 a[4], b[4], w[4], e[4];
+      unpack2<T, 8>(v[i], a);
+      unpack2<T, 8>(g[i], b);
+      unpack2<T, 8>(d[i], e);
       weights(i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = fmaf(rs, b[j] * w[j] - a[j] * rs * c, e[j]);
-      store_raw8<T, VEC>(dx + row * H + at.column(i), at.lane16, at.valid(i), pack<T, 8>(e));
+      for (int j = 0; j < 4; ++j) e[j] = add2(fma2(mul2(b[j], w[j]), rs2, mul2(a[j], by_h)), e[j]);
+      store_block8<T, VEC>(dx + row * H + at.column(i), at.lane16, at.valid(i), pack2<T, 8>(e));
     }
   }
   if (!part) return;
@@ -234,16 +221,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     if (r > 0) __syncthreads();
     if (at.group != r) continue;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < PER; ++i) {
+      float mine[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) gw[i][j].get(mine[2 * j], mine[2 * j + 1]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = block_column<VEC>(at.lane16, j);
         if (c < at.valid(i)) {
-          const float s = gw[i][j] + (r > 0 ? cols[at.column(i) + c] : 0.0f);
+          const float s = mine[j] + (r > 0 ? cols[at.column(i) + c] : 0.0f);
           if (r + 1 < at.rows) cols[at.column(i) + c] = s;
           else out[at.column(i) + c] = s;
         }
       }
+    }
   }
 }
 
@@ -282,7 +273,7 @@ struct RmsShape {
 RmsShape rms_shape(int H) {
   RmsShape s;
   s.nb = (H + MOE_BLOCK8 - 1) / MOE_BLOCK8;
-  s.per = s.nb <= 2 ? 1 : s.nb <= 4 ? 2 : 4;
+  s.per = s.nb <= 2 ? 1 : s.nb <= 56 ? 2 : 4;
   s.tpr = ((s.nb + s.per - 1) / s.per * 16 + 31) / 32 * 32;
   s.rows = std::max(1, 256 / s.tpr);
   s.most = 304 * (4 / s.per);
@@ -347,7 +338,7 @@ int moe_rmsnorm_forward(const moe_rmsnorm_config* cfg, const void* x, int64_t ld
     return with_rms(type, param_type, vec, r.per, [&](auto tv, auto pv, auto vv, auto n) {
       using T = decltype(tv);
       using P = decltype(pv);
-      return launch_pdl(rms_fwd_kernel<T, P, decltype(vv)::value, decltype(n)::value>, dim3(rms_blocks(c.N, r)),
+      return launch_pdl(rms_fwd_kernel<T, P, decltype(vv)::value, decltype(n)::value>, dim3((unsigned)(((int64_t)c.N + r.rows - 1) / r.rows)),
                         dim3(r.tpr * r.rows), 0, s, static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr,
                         static_cast<const P*>(weight), static_cast<T*>(h), static_cast<T*>(y), codes, scales, rstd, c.N,
                         c.H, r.nb, r.tpr, c.eps);
