@@ -451,53 +451,75 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
     // ------------------------------------------------------------ scales (both CTAs)
     // A tensor-memory column holds a row's scales of four K blocks; 128 rows are four columns of 32 lanes, so row
     // l + 32 i of the tile lies in word i of lane l's 16 bytes.
-    int slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int w = cluster; w < items && ok; w += clusters) {
-      const LinTile t = lin_tile<MODE, MX>(p, offs, first, w, total, shares);
-      const uint8_t* bs = p.b_scale + (int64_t)t.e * p.b_expert;
-      for (int kb = t.kb0; kb < t.kb1; kb += 4) {
-        const int left = t.kb1 - kb;
-        uint32_t a[4], b[2] = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    // The next four K blocks' bytes are loaded while these are laid out.
+    struct Bytes {
+      uint32_t a[4];   // of row lane + 32 i
+      uint32_t b;      // lanes 0..7: the byte of K block lane & 3, columns 128 (lane >> 2) .. of the tile
+    };
+    const bool words = ((reinterpret_cast<uintptr_t>(p.a_scale) | (uintptr_t)p.lda_s) & 3) == 0;
+    auto fetch = [&](const LinTile& t, int kb) {
+      Bytes v;
+      const int left = t.kb1 - kb;
+      const uint8_t* from = p.a_scale + (int64_t)(t.row0 + 128 * (int)rank + lane) * p.lda_s + kb;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 128 * (int)rank + lane + 32 * i;
-          a[i] = 0x7F7F7F7Fu;
-          if (r < t.rows) {
-            const uint8_t* s = p.a_scale + (int64_t)(t.row0 + r) * p.lda_s + kb;
+      for (int i = 0; i < 4; ++i, from += (int64_t)32 * p.lda_s) {
+        v.a[i] = 0x7F7F7F7Fu;
+        if (128 * (int)rank + lane + 32 * i < t.rows) {
+          if (words) {   // what lies past the last block is not used
+            v.a[i] = *reinterpret_cast<const uint32_t*>(from);
+          } else {
+            uint32_t x[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < left) a[i] = (a[i] & ~(0xFFu << (8 * j))) | (uint32_t)s[j] << (8 * j);
+            for (int j = 0; j < 4; ++j) x[j] = j < left ? from[j] : 127;
+            v.a[i] = x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24;
           }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (t.nt * 256 + 128 * h < p.cols) {
-            const uint8_t* s = bs + (int64_t)(2 * t.nt + h) * p.b_col + (int64_t)kb * p.b_k;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < left) b[h] = (b[h] & ~(0xFFu << (8 * j))) | (uint32_t)s[(int64_t)j * p.b_k] << (8 * j);
-          }
-        }
-        int good = 1;
-        if (lane == 0) good = wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, p.limit_ns, p.status, 805);
-        if (!__shfl_sync(0xffffffffu, good, 0)) {
-          ok = false;
-          break;
-        }
-        uint4* to = reinterpret_cast<uint4*>(smem + S::SF + slot * S::SF_BYTES);
-        to[lane] = make_uint4(a[0], a[1], a[2], a[3]);
-        to[32 + lane] = make_uint4(b[0], b[0], b[0], b[0]);
-        to[64 + lane] = make_uint4(b[1], b[1], b[1], b[1]);
-        fence_proxy_async_smem();                   // the copies to tensor memory read them
-        __syncwarp();
-        if (lane == 0) {
-          if (leader) mbar_arrive(sfull_bar(slot));
-          else mbar_arrive_cluster(mapa_shared(sfull_bar(slot), 0));
-        }
-        if (++slot == S::SF_SLOTS) { slot = 0; phase ^= 1u; }
       }
+      const int h = lane >> 2, j = lane & 3;
+      v.b = 127;
+      if (lane < 8 && j < left && t.nt * 256 + 128 * h < p.cols)
+        v.b = p.b_scale[(int64_t)t.e * p.b_expert + (int64_t)(2 * t.nt + h) * p.b_col + (int64_t)(kb + j) * p.b_k];
+      return v;
+    };
+    int slot = 0, w = cluster, kb = 0;
+    uint32_t phase = 0;
+    LinTile t = {};
+    // the first K block of the next tile that has one
+    auto next_tile = [&] {
+      for (; w < items; w += clusters) {
+        t = lin_tile<MODE, MX>(p, offs, first, w, total, shares);
+        kb = t.kb0;
+        if (kb < t.kb1) return;
+      }
+    };
+    next_tile();
+    Bytes now = {};
+    if (w < items) now = fetch(t, kb);
+    while (w < items) {
+      const Bytes v = now;
+      kb += 4;
+      if (kb >= t.kb1) {
+        w += clusters;
+        next_tile();
+      }
+      if (w < items) now = fetch(t, kb);
+      uint32_t b = v.b << (8 * (lane & 3));
+      b |= __shfl_xor_sync(0xffffffffu, b, 1);
+      b |= __shfl_xor_sync(0xffffffffu, b, 2);
+      const uint32_t b0 = __shfl_sync(0xffffffffu, b, 0), b1 = __shfl_sync(0xffffffffu, b, 4);
+      const bool good = wait_bounded(sempty_bar(slot), phase ^ 1u, abort_flag, p.limit_ns, p.status, 805);
+      if (!__all_sync(0xffffffffu, good)) break;
+      uint4* to = reinterpret_cast<uint4*>(smem + S::SF + slot * S::SF_BYTES);
+      to[lane] = make_uint4(v.a[0], v.a[1], v.a[2], v.a[3]);
+      to[32 + lane] = make_uint4(b0, b0, b0, b0);
+      to[64 + lane] = make_uint4(b1, b1, b1, b1);
+      fence_proxy_async_smem();                     // the copies to tensor memory read them
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(sfull_bar(slot));
+        else mbar_arrive_cluster(mapa_shared(sfull_bar(slot), 0));
+      }
+      if (++slot == S::SF_SLOTS) { slot = 0; phase ^= 1u; }
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
