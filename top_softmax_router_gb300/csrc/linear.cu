@@ -89,8 +89,8 @@ int moe_linear_forward(const moe_linear_config* cfg, const void* x, int64_t ldx,
   if (!ok16(x) || !ok16(w) || !ok16(y)) return MOE_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   LinMaps m = {};
-  const bool made = mx ? make_map_2d_u8(&m.a, x, c.K, c.N, ldx, 128, 128) && make_map_3d_u8(&m.b, w, c.K, c.O, c.E, 128, 128)
-                       : make_map_2d_strided(&m.a, x, c.K, c.N, ldx, 64, 128) && make_map_3d(&m.b, w, c.K, c.O, c.E, 64, 128);
+  const bool made = mx ? make_map_2d_u8(&m.a, x, c.K, c.N, ldx, 128, 128) && make_map_2d_u8(&m.few, x, c.K, c.N, ldx, 128, kFewRows) && make_map_3d_u8(&m.b, w, c.K, c.O, c.E, 128, 128)
+                       : make_map_2d_strided(&m.a, x, c.K, c.N, ldx, 64, 128) && make_map_2d_strided(&m.few, x, c.K, c.N, ldx, 64, kFewRows) && make_map_3d(&m.b, w, c.K, c.O, c.E, 64, 128);
   if (!made) return record_cuda_error(cudaErrorInvalidValue, "linear tensor maps");
   LinGemm p = linear_params(c, L, offsets, static_cast<uint8_t*>(ws));
   p.cols = c.O;
@@ -135,8 +135,8 @@ int moe_linear_backward(const moe_linear_config* cfg, const void* x, int64_t ldx
   const int ob = (int)up(c.O, MOE_BLOCK8), kb = (int)up(c.K, MOE_BLOCK8);
   if (dx) {
     LinMaps m = {};
-    const bool made = w8 ? make_map_2d_u8(&m.a, b + L.dy_codes, c.O, c.N, c.O, 128, 128) && make_map_3d_u8(&m.b, w, c.K, c.O, c.E, 128, 128)
-                         : make_map_2d(&m.a, dy, c.O, c.N, 64, 128) && make_map_3d(&m.b, w, c.K, c.O, c.E, 64, 64);
+    const bool made = w8 ? make_map_2d_u8(&m.a, b + L.dy_codes, c.O, c.N, c.O, 128, 128) && make_map_2d_u8(&m.few, b + L.dy_codes, c.O, c.N, c.O, 128, kFewRows) && make_map_3d_u8(&m.b, w, c.K, c.O, c.E, 128, 128)
+                         : make_map_2d(&m.a, dy, c.O, c.N, 64, 128) && make_map_2d(&m.few, dy, c.O, c.N, 64, kFewRows) && make_map_3d(&m.b, w, c.K, c.O, c.E, 64, 64);
     if (!made) return record_cuda_error(cudaErrorInvalidValue, "linear tensor maps");
     if (w8 && (v = timed_launch(MOE_K_BLOCKS8, "pack dy", s, [&] {
                  return launch_pack_rows(dy, c.O, MOE_TYPE_BF16, c.N, c.O, b + L.dy_codes, b + L.dy_scales, s);
@@ -160,11 +160,10 @@ int moe_linear_backward(const moe_linear_config* cfg, const void* x, int64_t ldx
   }
   if (!dw) return MOE_OK;
   const void* xv = x8 ? b + L.x_values : x;
-  LinMaps m = {};
-  if (!make_map_2d(&m.a, dy, c.O, c.N, 64, 64) || !make_map_2d(&m.a8, dy, c.O, c.N, 64, 8) || !make_map_2d(&m.a1, dy, c.O, c.N, 64, 1) ||
-      !make_map_2d_strided(&m.b, xv, c.K, c.N, ldx, 64, 64) || !make_map_2d_strided(&m.b8, xv, c.K, c.N, ldx, 64, 8) ||
-      !make_map_2d_strided(&m.b1, xv, c.K, c.N, ldx, 64, 1))
-    return record_cuda_error(cudaErrorInvalidValue, "linear tensor maps");
+  LinDwMaps m = {};
+  for (int i = 0; i < 7; ++i)
+    if (!make_map_2d(&m.a[i], dy, c.O, c.N, 64, 64 >> i) || !make_map_2d_strided(&m.b[i], xv, c.K, c.N, ldx, 64, 64 >> i))
+      return record_cuda_error(cudaErrorInvalidValue, "linear tensor maps");
   if (x8 && (v = timed_launch(MOE_K_BLOCKS8, "unpack x", s, [&] {
                return launch_unpack_rows(static_cast<const uint8_t*>(x), x_scales, c.N, c.K, b + L.x_values, MOE_TYPE_BF16, s);
              })) != MOE_OK)

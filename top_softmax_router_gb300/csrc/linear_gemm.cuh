@@ -34,9 +34,15 @@ namespace moe {
 enum LinMode : int { LIN_Y = 0, LIN_DX = 1, LIN_DW = 2 };
 
 struct LinMaps {
-  CUtensorMap a, b;                     // LIN_DW: boxes of 64 rows
-  CUtensorMap a8, a1, b8, b1;           // LIN_DW: the same matrices in boxes of 8 rows and of one
+  CUtensorMap a, b;
+  CUtensorMap few;                      // LIN_Y, LIN_DX: A in boxes of kFewRows rows
 };
+// LIN_DW: both matrices in boxes of 64, 32, .. 1 rows.
+struct LinDwMaps {
+  CUtensorMap a[7], b[7];
+};
+template <int MODE>
+using LinMapsOf = std::conditional_t<MODE == LIN_DW, LinDwMaps, LinMaps>;
 
 struct LinGemm {
   int n, E;                  // rows of x and dy; experts
@@ -62,6 +68,7 @@ struct LinGemm {
 
 constexpr int kLinClusters = 76;   // at most this many clusters run (two dies x 76 SMs in pairs)
 constexpr int kLinBand = 8;        // row tiles that are worked on together: their rows and a few column tiles of W stay in L2
+constexpr int kFewRows = 32;       // tiles of no more rows load no more of A (x of another expert would come with them)
 // The tensor cores cut each addition to an accumulator off towards zero: dW sums 1024 rows to an accumulator and adds
 // those in fp32 registers, so that the loss does not grow with the rows.
 constexpr int kDwShare = 16;       // K blocks of 64 rows
@@ -197,7 +204,7 @@ __device__ __forceinline__ void lin_store16(const LinGemm& p, int64_t at, const 
 
 template <int MODE, bool MX>
 __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
-    linear_gemm_kernel(const __grid_constant__ LinMaps maps, const LinGemm p) {
+    linear_gemm_kernel(const __grid_constant__ LinMapsOf<MODE> maps, const LinGemm p) {
   static_assert(!(MX && MODE == LIN_DW), "dW takes bf16 operands");
   using S = LinSmem;
   constexpr bool A_MN = MODE == LIN_DW, B_MN = MODE != LIN_Y;
@@ -244,8 +251,7 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&maps.a);
-    tma_prefetch_desc(&maps.b);
+    tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&maps));
   }
   if (warp == 1) {
     tc_alloc_pair(smem_u32(tmem_slot), 512);
@@ -314,37 +320,41 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
             const int orow = t.mt * 256 + 128 * (int)rank;
             if (left >= 64) {
               if (leader) mbar_expect_tx(full_bar(stage), 2 * S::STAGE);
-              tma_load_2d_pair(sa, &maps.a, fb, orow, r);
-              tma_load_2d_pair(sa + 8192, &maps.a, fb, orow + 64, r);
-              tma_load_2d_pair(sb, &maps.b, fb, col, r);
-              tma_load_2d_pair(sb + 8192, &maps.b, fb, col + 64, r);
+              tma_load_2d_pair(sa, &maps.a[0], fb, orow, r);
+              tma_load_2d_pair(sa + 8192, &maps.a[0], fb, orow + 64, r);
+              tma_load_2d_pair(sb, &maps.b[0], fb, col, r);
+              tma_load_2d_pair(sb + 8192, &maps.b[0], fb, col + 64, r);
             } else {
               // The last rows, and zeros up to a multiple of 16, an MMA's share: what follows is another expert's (or
-              // nobody's, and no number).  Eight rows at a time, then one; a row past the matrix reads as zeros.
+              // nobody's, and no number).  In boxes of a power of two of rows each, the zeros from past the matrix.
               const int up = (left + 15) & ~15;
               if (leader) mbar_expect_tx(full_bar(stage), 2 * 4 * 128 * up);
-              for (int j = 0; j < up; j += 8) {
+              int j = 0;
+              auto box = [&](const CUtensorMap* ma, const CUtensorMap* mb, int rows, int at) {
                 const uint32_t da = sa + j * 128, db = sb + j * 128;
-                if (j + 8 <= left || j >= left) {
-                  const int at = j < left ? r + j : p.n;
-                  tma_load_2d_pair(da, &maps.a8, fb, orow, at);
-                  tma_load_2d_pair(da + 8192, &maps.a8, fb, orow + 64, at);
-                  tma_load_2d_pair(db, &maps.b8, fb, col, at);
-                  tma_load_2d_pair(db + 8192, &maps.b8, fb, col + 64, at);
-                } else {
-                  for (int i = 0; i < 8; ++i) {
-                    const int at = j + i < left ? r + j + i : p.n;
-                    tma_load_2d_pair(da + i * 128, &maps.a1, fb, orow, at);
-                    tma_load_2d_pair(da + i * 128 + 8192, &maps.a1, fb, orow + 64, at);
-                    tma_load_2d_pair(db + i * 128, &maps.b1, fb, col, at);
-                    tma_load_2d_pair(db + i * 128 + 8192, &maps.b1, fb, col + 64, at);
-                  }
-                }
-              }
+                tma_load_2d_pair(da, ma, fb, orow, at);
+                tma_load_2d_pair(da + 8192, ma, fb, orow + 64, at);
+                tma_load_2d_pair(db, mb, fb, col, at);
+                tma_load_2d_pair(db + 8192, mb, fb, col + 64, at);
+                j += rows;
+              };
+#pragma unroll
+              for (int i = 1; i < 7; ++i)
+                if (left & (64 >> i)) box(&maps.a[i], &maps.b[i], 64 >> i, r + j);
+#pragma unroll
+              for (int i = 6; i > 2; --i)
+                if ((up - left) & (64 >> i)) box(&maps.a[i], &maps.b[i], 64 >> i, p.n);
             }
           } else {
-            if (leader) mbar_expect_tx(full_bar(stage), 2 * S::STAGE);
-            tma_load_2d_pair(sa, &maps.a, fb, k0, t.row0 + 128 * (int)rank);
+            if (t.rows <= kFewRows) {   // the rows past them, in the even CTA and all of the odd one's, go to no output
+              if (leader) {
+                mbar_expect_tx(full_bar(stage), 2 * S::HALF + kFewRows * 128);
+                tma_load_2d_pair(sa, &maps.few, fb, k0, t.row0);
+              }
+            } else {
+              if (leader) mbar_expect_tx(full_bar(stage), 2 * S::STAGE);
+              tma_load_2d_pair(sa, &maps.a, fb, k0, t.row0 + 128 * (int)rank);
+            }
             if constexpr (!B_MN) {
               tma_load_3d_pair(sb, &maps.b, fb, k0, col, t.e);
             } else if constexpr (MX) {
@@ -566,7 +576,7 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
         if (c >= width || !some) return;
         if (shares == 1) {
           if (in) lin_store16(p, row * p.cols + c0 + c, v);
-        } else {
+        } else if (in) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             part[(c / 4 + j) * 32] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -645,23 +655,38 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
         if (lane == 0) before = atomicInc(p.done + (tile * 2 + (int)rank) * 8 + (warp - 2), (unsigned)shares - 1);
         before = __shfl_sync(0xffffffffu, before, 0);
         if (before == (unsigned)shares - 1) {
+          // Few rows are spread over the lanes: item i is four columns, i / wide, of row i % wide.  16 loads in flight.
           __threadfence();
+          const int rows = __popc(__ballot_sync(0xffffffffu, in));     // the first ones
+          const int log_wide = 32 - __clz(rows - 1), wide = 1 << log_wide;
+          const int64_t row0 = row - lane;
+          const float4* from = reinterpret_cast<const float4*>(p.part + ((int64_t)(tile * 2 + (int)rank) * 8 + (warp - 2)) * 4096);
+          const int64_t next = (int64_t)total * 16 * 1024;             // a share further, in float4
 #pragma unroll 1
-          for (int c = 0; c < width; c += 16) {
-            float v[16];
+          for (int k = 0; k < wide; k += 8) {
+            float4 v[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-#pragma unroll 1
+            for (int j = 0; j < 8; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
             for (int s = 0; s < shares; ++s) {
-              const float4* from = reinterpret_cast<const float4*>(
-                  p.part + ((int64_t)((s * total + tile) * 2 + (int)rank) * 8 + (warp - 2)) * 4096) + lane;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 x = __ldcg(from + (c / 4 + j) * 32);
-                v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
+              for (int j = 0; j < 8; ++j) {
+                const int i = lane + 32 * (k + j), c = i >> log_wide;
+                if (k + j < wide && 4 * c < width) {
+                  const float4 x = __ldcg(from + s * next + c * 32 + (i & (wide - 1)));
+                  v[j].x += x.x, v[j].y += x.y, v[j].z += x.z, v[j].w += x.w;
+                }
               }
             }
-            if (in) lin_store16(p, row * p.cols + c0 + c, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int i = lane + 32 * (k + j), c = i >> log_wide, r = i & (wide - 1);
+              if (k + j < wide && 4 * c < width && r < rows) {
+                const int64_t at = (row0 + r) * p.cols + c0 + 4 * c;
+                if (p.out32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v[j];
+                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16(v[j].x, v[j].y), pack_bf16(v[j].z, v[j].w));
+              }
+            }
           }
         }
       }
@@ -675,7 +700,7 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
 }
 
 template <int MODE, bool MX>
-cudaError_t launch_linear_gemm(const LinMaps& maps, LinGemm p, int sms, cudaStream_t s) {
+cudaError_t launch_linear_gemm(const LinMapsOf<MODE>& maps, LinGemm p, int sms, cudaStream_t s) {
   auto kern = linear_gemm_kernel<MODE, MX>;
   p.sectors = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   const int smem = LinSmem::total(p.E);

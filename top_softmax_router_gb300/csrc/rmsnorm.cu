@@ -14,9 +14,9 @@
 namespace moe {
 namespace {
 
-// Two blocks of 448 threads of the forward share a SM; rows wider than 7168 take one block of up to 512.
-constexpr int rms_threads(int per) { return per <= 2 ? 448 : 512; }
-constexpr int rms_resident(int per) { return per <= 2 ? 2 : 1; }
+// Most threads of a block; the backward takes two blocks of 128 columns a half warp up to 7168 columns.
+constexpr int kFwdThreads = 512;
+constexpr int bwd_threads(int per) { return per <= 2 ? 448 : 512; }
 constexpr int kMaxRows = 8;
 
 // A row's warps leave their sums here, in turn, so that one barrier a row suffices; places without a warp hold 0.
@@ -56,7 +56,7 @@ struct RowPlace {
 };
 
 template <class T, class P, bool VEC, int PER>
-__global__ void __launch_bounds__(rms_threads(PER), rms_resident(PER))
+__global__ void __launch_bounds__(kFwdThreads, 1)
     rms_fwd_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ res, int64_t ldr,
                    const P* __restrict__ weight, T* __restrict__ h, T* __restrict__ y, uint8_t* __restrict__ codes,
                    uint8_t* __restrict__ scales, float* __restrict__ rstd, int N, int H, int nb, int tpr, float eps) {
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(rms_threads(PER), rms_resident(PER))
 // Each thread keeps the sums of dy xh of its columns in registers over all its rows.  The row groups of a block add
 // theirs up in order, into part[block][H]; rms_param_kernel adds the blocks in order.
 template <class T, class P, bool VEC, int PER>
-__global__ void __launch_bounds__(rms_threads(PER), 1)
+__global__ void __launch_bounds__(bwd_threads(PER), 1)
     rms_bwd_kernel(const T* __restrict__ h, int64_t ldh, const P* __restrict__ weight, const float* __restrict__ rstd,
                    const T* __restrict__ dy, int64_t lddy, const T* __restrict__ dh, int64_t lddh, T* __restrict__ dx,
                    float* __restrict__ part, int N, int H, int tpr) {
@@ -146,20 +146,21 @@ __global__ void __launch_bounds__(rms_threads(PER), 1)
   for (int i = 0; i < PER; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) gw[i][j] = f32x2(0.0f);
-  Pack<T, 8> nh[PER], ng[PER];
+  Pack<T, 8> nh[PER], ng[PER], nd[PER];
   float rs_next = 0.0f;
+  auto load_dh = [&](int64_t row, int i) {
+    const int n = row < N && dx && dh ? at.valid(i) : 0;
+    return load_block8<T, VEC>(n ? dh + row * lddh + at.column(i) : h, at.lane16, n);
+  };
   auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int v = row < N ? at.valid(i) : 0;
       nh[i] = load_block8<T, VEC>(h + (v ? row * ldh + at.column(i) : 0), at.lane16, v);
       ng[i] = load_block8<T, VEC>(dy + (v ? row * lddy + at.column(i) : 0), at.lane16, v);
+      if (!LATE) nd[i] = load_dh(row, i);
     }
     rs_next = row < N ? rstd[row] : 0.0f;
-  };
-  auto load_dh = [&](int64_t row, int i) {
-    const int n = row < N && dx && dh ? at.valid(i) : 0;
-    return load_block8<T, VEC>(n ? dh + row * lddh + at.column(i) : h, at.lane16, n);
   };
   // Read again for each use, from L1: held, the weights of a row would take the registers of the next row.
   auto weights = [&](int i, f32x2 (&f)[4]) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(rms_threads(PER), 1)
     for (int i = 0; i < PER; ++i) {
       v[i] = nh[i];
       g[i] = ng[i];
-      if (!LATE) d[i] = load_dh(row, i);
+      d[i] = nd[i];
     }
     if (AHEAD) load(row + (int64_t)gridDim.x * at.rows);
 #pragma unroll
@@ -270,10 +271,10 @@ int rms_validate(const moe_rmsnorm_config* c) {
 struct RmsShape {
   int nb, per, tpr, rows, most;
 };
-RmsShape rms_shape(int H) {
+RmsShape rms_shape(int H, bool forward) {
   RmsShape s;
   s.nb = (H + MOE_BLOCK8 - 1) / MOE_BLOCK8;
-  s.per = s.nb <= 2 ? 1 : s.nb <= 56 ? 2 : 4;
+  s.per = s.nb <= 2 ? 1 : s.nb <= (forward ? 4 : 56) ? 2 : 4;
   s.tpr = ((s.nb + s.per - 1) / s.per * 16 + 31) / 32 * 32;
   s.rows = std::max(1, 256 / s.tpr);
   s.most = 304 * (4 / s.per);
@@ -312,7 +313,7 @@ extern "C" {
 int moe_rmsnorm_workspace_bytes(const moe_rmsnorm_config* cfg, size_t* bwd_bytes) {
   const int v = rms_validate(cfg);
   if (v != MOE_OK) return v;
-  if (bwd_bytes) *bwd_bytes = sizeof(WsHeader) + align256((size_t)rms_blocks(cfg->N, rms_shape(cfg->H)) * cfg->H * 4);
+  if (bwd_bytes) *bwd_bytes = sizeof(WsHeader) + align256((size_t)rms_blocks(cfg->N, rms_shape(cfg->H, false)) * cfg->H * 4);
   return MOE_OK;
 }
 
@@ -331,7 +332,7 @@ int moe_rmsnorm_forward(const moe_rmsnorm_config* cfg, const void* x, int64_t ld
   if (c.N == 0) return MOE_OK;
   if (!x || !aligned_to(x, ts)) return MOE_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RmsShape r = rms_shape(c.H);
+  const RmsShape r = rms_shape(c.H, true);
   const bool vec = c.H % 8 == 0 && vec_rows(x, ldx, type) && vec_rows(residual, ldr, type) && vec_rows(h, c.H, type) &&
                    vec_rows(y, c.H, type) && aligned_to(weight, 16) && aligned_to(codes, 8);
   return timed_launch(MOE_K_RMS_FWD, "rms norm", s, [&] {
@@ -370,7 +371,7 @@ int moe_rmsnorm_backward(const moe_rmsnorm_config* cfg, const void* h, int64_t l
   moe_rmsnorm_workspace_bytes(cfg, &need);
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!dx && !dweight) return MOE_OK;
-  const RmsShape r = rms_shape(c.H);
+  const RmsShape r = rms_shape(c.H, false);
   const bool vec = c.H % 8 == 0 && vec_rows(h, ldh, type) && vec_rows(dy, lddy, type) && vec_rows(dh, lddh, type) &&
                    vec_rows(dx, c.H, type) && aligned_to(weight, 16);
   float* part = dweight ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader)) : nullptr;
