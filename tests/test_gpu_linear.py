@@ -253,3 +253,18 @@ def test_large_offsets(M):
     ref, size = R.linear(host(x[-5:]), host(w), [0, 2, 5])
     near(y[-5:], ref, size, K, 2.0 ** -8)
     assert torch.all(y[:-256] == 0)
+
+
+def test_a_thread_of_its_own(M):
+    """The first call of a thread that has used no CUDA yet (as autograd's has not), and two threads in turn."""
+    import threading
+    c = Case(M, 70, 272, 144, ends([40, 30]), x8=True, w8=True)
+    u = c.unit(M)
+    want, got = check(M, c, u), []
+    stream = torch.cuda.current_stream()
+    for _ in range(2):
+        t = threading.Thread(target=lambda: got.append((u.forward(c.x, c.w, c.off, c.xs, c.ws, stream=stream),
+                                                        *u.backward(c.x, c.w, c.dy, c.off, c.xs, c.ws, stream=stream))))
+        t.start()
+        t.join()
+    assert len(got) == 2 and all(torch.equal(p, q) for g in got for p, q in zip(g, want))

@@ -14,14 +14,17 @@ import functools
 import torch
 
 from .api import MoEBlock
+from .blocks8 import Checkpoint8, Checkpoint8Config, pack_weight8
 from .ce import VocabCE
 from .distill import VocabDistill
 from .embed import TokenEmbedding
+from .linear import ExpertLinear
 from .norm import LayerNorm
+from .rmsnorm import RMSNorm
 from .scores import ScoreRouter
 
 __all__ = ["MoEFunction", "VocabCEFunction", "moe_block", "vocab_cross_entropy", "moe_experts", "expert_scores",
-           "layer_norm", "token_embedding", "vocab_distill"]
+           "layer_norm", "token_embedding", "vocab_distill", "rms_norm", "expert_linear", "rms_norm_linear8"]
 
 
 class _Final(torch.autograd.Function):
@@ -216,3 +219,103 @@ class _Distill(torch.autograd.Function):
 def vocab_distill(X, W, ids, teacher, unit: VocabDistill):
     """Differentiable mean distillation loss of the head X W^T against a teacher's top logits."""
     return _Distill.apply(X, W, ids, teacher, unit)
+
+
+def _none_or_rows(t):
+    return None if t is None else _dense_rows(t)
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, unit):
+        y, h, rstd, _, _ = unit.forward(x, weight, residual)
+        ctx.unit = unit
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, weight, rstd)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dy = torch.zeros_like(h) if dy is None else _dense_rows(dy)
+        dx, dw = ctx.unit.backward(h, weight, rstd, dy, _none_or_rows(dh), want_dx=need[0] or need[1],
+                                   want_dweight=need[2])
+        return dx if need[0] else None, dx if need[1] else None, dw if dw is None else dw.to(weight.dtype), None
+
+
+def rms_norm(x, weight, unit: RMSNorm, residual=None):
+    """Differentiable RMS norm over an RMSNorm's workspace: y, or with a residual (y, h), h = x + residual."""
+    return _RMSNorm.apply(x, residual, weight, unit)
+
+
+class _ExpertLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets, unit, keep):
+        xs = ws = None
+        kept, held = x, w
+        if keep != "bf16":
+            kept, xs = Checkpoint8(Checkpoint8Config(N=unit.cfg.N, H=unit.cfg.K)).pack(x)
+        if keep == "blocks8":
+            held, ws = pack_weight8(w)
+            y = unit.forward(kept, held, offsets, xs, ws)
+        else:
+            y = unit.forward(x, w, offsets)
+        ctx.unit, ctx.type = unit, w.dtype
+        ctx.save_for_backward(kept, xs, held, ws, offsets)
+        return y
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy):
+        x, xs, w, ws, offsets = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw = ctx.unit.backward(x, w, dy.contiguous(), offsets, xs, ws, want_dx=need[0], want_dw=need[1],
+                                   dw_dtype=ctx.type)
+        return dx, dw, None, None, None
+
+
+def expert_linear(x, w, unit: ExpertLinear, offsets=None, keep="bf16"):
+    """Differentiable product by expert over an ExpertLinear's workspace, x [n, K] and w [E, O, K] in bf16.  keep: "bf16"
+    keeps x for the backward pass, "checkpoint8" keeps it in 8 bits (which dw then takes it from), "blocks8" also computes
+    y and dx in 8 bits, with w and dy packed in each pass (the two need a unit made with blocks8)."""
+    if keep not in ("bf16", "checkpoint8", "blocks8"):
+        raise ValueError("keep: expected 'bf16', 'checkpoint8' or 'blocks8'")
+    return _ExpertLinear.apply(x, w, offsets, unit, keep)
+
+
+class _RMSNormLinear8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, w, offsets, norm, linear):
+        _, h, rstd, codes, scales = norm.forward(x, weight, residual, want_y=False, want_codes=True)
+        wc, ws = pack_weight8(w)
+        out = linear.forward(codes, wc, offsets, scales, ws)
+        ctx.norm, ctx.linear, ctx.type = norm, linear, w.dtype
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, weight, rstd, codes, scales, wc, ws, offsets)
+        return out if residual is None else (out, h)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout, dh=None):
+        h, weight, rstd, codes, scales, wc, ws, offsets = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        rows = need[0] or need[1]
+        if dout is None:
+            dout = torch.zeros(h.shape[0], wc.shape[1], dtype=torch.bfloat16, device=h.device)
+        dy, dw = ctx.linear.backward(codes, wc, dout.contiguous(), offsets, scales, ws, want_dx=rows or need[2],
+                                     want_dw=need[3], dw_dtype=ctx.type)
+        dx = dweight = None
+        if rows or need[2]:
+            dx, dweight = ctx.norm.backward(h, weight, rstd, dy, _none_or_rows(dh), want_dx=rows, want_dweight=need[2])
+        return (dx if need[0] else None, dx if need[1] else None,
+                dweight if dweight is None else dweight.to(weight.dtype), dw, None, None, None)
+
+
+def rms_norm_linear8(x, weight, w, norm: RMSNorm, linear: ExpertLinear, residual=None, offsets=None):
+    """The product by expert, in 8 bits, of an RMS norm's output, which is never written but in 8 bits (and kept so for
+    the backward pass): out, or with a residual (out, h).  x, residual and w in bf16; `linear` made with blocks8."""
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x: expected bfloat16")
+    return _RMSNormLinear8.apply(x, residual, weight, w, offsets, norm, linear)

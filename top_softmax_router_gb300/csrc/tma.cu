@@ -32,9 +32,17 @@ static bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, dtype, rank, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, MOE_TMA_L2_PROMOTION,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto call = [&] {
+    return fn(m, dtype, rank, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, MOE_TMA_L2_PROMOTION, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = call();
+  if (r != CUDA_SUCCESS) {
+    // A thread that has made no runtime call yet (autograd's, say) has no current context, which the driver's entry
+    // point needs; setting the device makes its primary context current.
+    int device = 0;
+    if (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = call();
+  }
   return r == CUDA_SUCCESS;
 }
 
