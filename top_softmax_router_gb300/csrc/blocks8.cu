@@ -1,7 +1,10 @@
 // Matrices in 8 bits with a scale for each block of 128 (include/moe_blocks8.h): packing of rows and of weights, unpacking.
 //
 // All three are one pass over memory: 2 + 1 + 1/128 bytes a bf16 value.  A half warp holds a row's block of 128, eight
-// values a lane (16 bytes of bf16), and finds its largest magnitude by four shuffles.
+// values a lane (16 bytes of bf16), and finds its largest magnitude by four shuffles; four blocks side by side keep enough
+// loads in flight.  A block's row comes from a multiplication (divisions of 64 bits and the tests for infinities of every
+// value held the pair of passes below at 443 us).  65536 x 4096 bf16, packed and restored: 257 us, 6.3 TB/s of the
+// measured 6.8.
 #include <algorithm>
 
 #include "../../include/moe_blocks8.h"
