@@ -14,8 +14,9 @@
 namespace moe {
 namespace {
 
-// Most threads of a block; the backward takes two blocks of 128 columns a half warp up to 7168 columns.
-constexpr int kFwdThreads = 512;
+// Most threads of a block.  Up to 7168 columns the forward has four blocks of 224 threads a SM (72 registers; with 78, and
+// three blocks, 32768 x 7168 took 424 us for 365), the backward two blocks of 128 columns a half warp.
+constexpr int kFwdThreads = 224, kFwdWide = 512;
 constexpr int bwd_threads(int per) { return per <= 2 ? 448 : 512; }
 constexpr int kMaxRows = 8;
 
@@ -53,10 +54,34 @@ struct RowPlace {
   __device__ __forceinline__ int column(int i) const { return block(i) * MOE_BLOCK8; }
   __device__ __forceinline__ int step() const { return hws * MOE_BLOCK8; }
   __device__ __forceinline__ int valid(int i) const { return max(0, min(MOE_BLOCK8, H - column(i))); }
+  // What a thread asks of block i before it touches it, worked out once: with VEC whether its eight are in the row, else
+  // how many of the block's columns are.  Pointers start at first(): the thread's eight, or the block.
+  template <bool VEC>
+  __device__ __forceinline__ int in(int i) const { return VEC ? lane16 * 8 < valid(i) : valid(i); }
+  template <bool VEC>
+  __device__ __forceinline__ int first() const { return column(0) + (VEC ? lane16 * 8 : 0); }
 };
+template <class T, bool VEC>
+__device__ __forceinline__ Pack<T, 8> get8(const T* p, int lane16, int in) {
+  if constexpr (VEC) {
+    Pack<T, 8> a = zero_pack<T, 8>();
+    if (in) a = load_pack<T, 8>(p);
+    return a;
+  } else {
+    return load_block8<T, false>(p, lane16, in);
+  }
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void put8(T* p, int lane16, int in, const Pack<T, 8>& a) {
+  if constexpr (VEC) {
+    if (in) store_pack<T, 8>(p, a);
+  } else {
+    store_block8<T, false>(p, lane16, in, a);
+  }
+}
 
-template <class T, class P, bool VEC, int PER>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+template <class T, class P, bool VEC, int PER, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kFwdWide : kFwdThreads, WIDE ? 1 : 4)
     rms_fwd_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ res, int64_t ldr,
                    const P* __restrict__ weight, T* __restrict__ h, T* __restrict__ y, uint8_t* __restrict__ codes,
                    uint8_t* __restrict__ scales, float* __restrict__ rstd, int N, int H, int nb, int tpr, float eps) {
@@ -66,17 +91,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const RowPlace at(tpr, H);
   const int64_t row = (int64_t)blockIdx.x * at.rows + at.group;
   const bool there = row < N;        // of a row group, so of whole warps
+  int in[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) in[i] = at.template in<VEC>(i);
+  const int first = at.template first<VEC>(), step = at.step();
   Pack<T, 8> v[PER];
-  const T* xr = x + (there ? row * ldx : 0) + at.column(0);
-  const T* rr = res + (there ? row * ldr : 0) + at.column(0);
+  const T* xr = x + (there ? row * ldx : 0) + first;
+  const T* rr = res + (there ? row * ldr : 0) + first;
   f32x2 sq(0.0f);
   {
     Pack<T, 8> r[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int n = there ? at.valid(i) : 0;
-      v[i] = load_block8<T, VEC>(xr + i * at.step(), at.lane16, n);
-      if (res) r[i] = load_block8<T, VEC>(rr + i * at.step(), at.lane16, n);
+      v[i] = get8<T, VEC>(xr + i * step, at.lane16, there ? in[i] : 0);
+      if (res) r[i] = get8<T, VEC>(rr + i * step, at.lane16, there ? in[i] : 0);
     }
     if (tpr > 32) clear(sums);
 #pragma unroll
@@ -98,21 +126,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const float rs = 1.0f / sqrtf(row_sum(sq.sum(), tpr, at.group, at.t, sums.v[0]) * (1.0f / (float)H) + eps);
   if (!there) return;
   if (rstd && at.t == 0) rstd[row] = rs;
-  const int64_t to = row * H + at.column(0);
+  const int64_t to = row * H + first;
   const f32x2 rs2(rs);
   f32x2 f[PER][4];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int n = at.valid(i);
-    if (h) store_block8<T, VEC>(h + to + i * at.step(), at.lane16, n, v[i]);
-    f32x2 g[4];
-    Pack<P, 8> w = one_pack<P, 8>();
-    if (weight && n) w = load_block8<P, VEC>(weight + at.column(i), at.lane16, n);
+    if (h) put8<T, VEC>(h + to + i * step, at.lane16, in[i], v[i]);
     unpack2<T, 8>(v[i], f[i]);
-    unpack2<P, 8>(w, g);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], rs2), g[j]);
-    if (y) store_block8<T, VEC>(y + to + i * at.step(), at.lane16, n, pack2<T, 8>(f[i]));
+    for (int j = 0; j < 4; ++j) f[i][j] = mul2(f[i][j], rs2);
+    if (weight) {
+      f32x2 g[4];
+      unpack2<P, 8>(get8<P, VEC>(weight + first + i * step, at.lane16, in[i]), g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[i][j] = mul2(f[i][j], g[j]);
+    }
+    if (y) put8<T, VEC>(y + to + i * step, at.lane16, in[i], pack2<T, 8>(f[i]));
   }
   if (!codes) return;
   float m[PER];
@@ -120,8 +149,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int byte = block_scale_byte(m[i]);
-    store_codes8<VEC>(codes + to + i * at.step(), at.lane16, at.valid(i), block_codes(f[i], byte, infinite));
-    if (at.valid(i) && at.lane16 == 0) scales[row * nb + at.block(i)] = (uint8_t)byte;
+    const uint2 c = block_codes(f[i], byte, infinite);
+    if constexpr (VEC) {
+      if (in[i]) *reinterpret_cast<uint2*>(codes + to + i * step) = c;
+    } else {
+      store_codes8<false>(codes + to + i * step, at.lane16, in[i], c);
+    }
+    if (in[i] && at.lane16 == 0) scales[row * nb + at.block(i)] = (uint8_t)byte;
   }
 }
 
@@ -146,33 +180,45 @@ __global__ void __launch_bounds__(bwd_threads(PER), 1)
   for (int i = 0; i < PER; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) gw[i][j] = f32x2(0.0f);
+  int in[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) in[i] = at.template in<VEC>(i);
+  const int first = at.template first<VEC>(), step = at.step();
+  const int64_t row0 = (int64_t)blockIdx.x * at.rows + at.group, jump = (int64_t)gridDim.x * at.rows;
+  const T* hp = h + row0 * ldh + first;       // of the row that is loaded next
+  const T* gp = dy + row0 * lddy + first;
+  const T* dp = dh + row0 * lddh + first;     // only read where there is a dh
+  const bool with_dh = dx && dh;
   Pack<T, 8> nh[PER], ng[PER], nd[PER];
   float rs_next = 0.0f;
-  auto load_dh = [&](int64_t row, int i) {
-    const int n = row < N && dx && dh ? at.valid(i) : 0;
-    return load_block8<T, VEC>(n ? dh + row * lddh + at.column(i) : h, at.lane16, n);
-  };
   auto load = [&](int64_t row) {
+    const bool there = row < N;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int v = row < N ? at.valid(i) : 0;
-      nh[i] = load_block8<T, VEC>(h + (v ? row * ldh + at.column(i) : 0), at.lane16, v);
-      ng[i] = load_block8<T, VEC>(dy + (v ? row * lddy + at.column(i) : 0), at.lane16, v);
-      if (!LATE) nd[i] = load_dh(row, i);
+      nh[i] = get8<T, VEC>(hp + i * step, at.lane16, there ? in[i] : 0);
+      ng[i] = get8<T, VEC>(gp + i * step, at.lane16, there ? in[i] : 0);
+      if (!LATE) nd[i] = get8<T, VEC>(dp + i * step, at.lane16, there && with_dh ? in[i] : 0);
     }
-    rs_next = row < N ? rstd[row] : 0.0f;
+    rs_next = there ? rstd[row] : 0.0f;
+    hp += jump * ldh;
+    gp += jump * lddy;
+    if (!LATE) dp += jump * lddh;
   };
   // Read again for each use, from L1: held, the weights of a row would take the registers of the next row.
   auto weights = [&](int i, f32x2 (&f)[4]) {
     const P* p = weight;
     asm volatile("" : "+l"(p));
-    Pack<P, 8> raw = one_pack<P, 8>();
-    if (p && at.valid(i)) raw = load_block8<P, VEC>(p + at.column(i), at.lane16, at.valid(i));
-    unpack2<P, 8>(raw, f);
+    if (p) {
+      unpack2<P, 8>(get8<P, VEC>(p + first + i * step, at.lane16, in[i]), f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = f32x2(1.0f);
+    }
   };
-  if (AHEAD) load((int64_t)blockIdx.x * at.rows + at.group);
+  T* op = dx + row0 * H + first;
+  if (AHEAD) load(row0);
   int it = 0;
-  for (int64_t base = (int64_t)blockIdx.x * at.rows; base < N; base += (int64_t)gridDim.x * at.rows, ++it) {
+  for (int64_t base = (int64_t)blockIdx.x * at.rows; base < N; base += jump, ++it, op += jump * H) {
     const int64_t row = base + at.group;
     if (!AHEAD) load(row);
     Pack<T, 8> v[PER], g[PER], d[PER];
@@ -185,7 +231,7 @@ __global__ void __launch_bounds__(bwd_threads(PER), 1)
       g[i] = ng[i];
       d[i] = nd[i];
     }
-    if (AHEAD) load(row + (int64_t)gridDim.x * at.rows);
+    if (AHEAD) load(row + jump);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       f32x2 a[4], b[4], w[4];
@@ -201,20 +247,22 @@ __global__ void __launch_bounds__(bwd_threads(PER), 1)
     }
     if (!dx) continue;               // all threads alike
     const float c = row_sum(sum.sum(), tpr, at.group, at.t, sums.v[it & 1]) * inv_h;
-    if (row >= N) continue;
-    const f32x2 by_h(-rs * rs * c);
+    if (row < N) {
+      const f32x2 by_h(-rs * rs * c);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (LATE) d[i] = load_dh(row, i);
-      f32x2 a[4], b[4], w[4], e[4];
-      unpack2<T, 8>(v[i], a);
-      unpack2<T, 8>(g[i], b);
-      unpack2<T, 8>(d[i], e);
-      weights(i, w);
+      for (int i = 0; i < PER; ++i) {
+        if (LATE) d[i] = get8<T, VEC>(dp + i * step, at.lane16, with_dh ? in[i] : 0);
+        f32x2 a[4], b[4], w[4], e[4];
+        unpack2<T, 8>(v[i], a);
+        unpack2<T, 8>(g[i], b);
+        unpack2<T, 8>(d[i], e);
+        weights(i, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = add2(fma2(mul2(b[j], w[j]), rs2, mul2(a[j], by_h)), e[j]);
-      store_block8<T, VEC>(dx + row * H + at.column(i), at.lane16, at.valid(i), pack2<T, 8>(e));
+        for (int j = 0; j < 4; ++j) e[j] = add2(fma2(mul2(b[j], w[j]), rs2, mul2(a[j], by_h)), e[j]);
+        put8<T, VEC>(op + i * step, at.lane16, in[i], pack2<T, 8>(e));
+      }
     }
+    if (LATE) dp += jump * lddh;
   }
   if (!part) return;
   float* out = part + (int64_t)blockIdx.x * H;
@@ -276,7 +324,7 @@ RmsShape rms_shape(int H, bool forward) {
   s.nb = (H + MOE_BLOCK8 - 1) / MOE_BLOCK8;
   s.per = s.nb <= 2 ? 1 : s.nb <= (forward ? 4 : 56) ? 2 : 4;
   s.tpr = ((s.nb + s.per - 1) / s.per * 16 + 31) / 32 * 32;
-  s.rows = std::max(1, 256 / s.tpr);
+  s.rows = std::max(1, (forward ? kFwdThreads : 256) / s.tpr);
   s.most = 304 * (4 / s.per);
   return s;
 }
@@ -339,7 +387,11 @@ int moe_rmsnorm_forward(const moe_rmsnorm_config* cfg, const void* x, int64_t ld
     return with_rms(type, param_type, vec, r.per, [&](auto tv, auto pv, auto vv, auto n) {
       using T = decltype(tv);
       using P = decltype(pv);
-      return launch_pdl(rms_fwd_kernel<T, P, decltype(vv)::value, decltype(n)::value>, dim3((unsigned)(((int64_t)c.N + r.rows - 1) / r.rows)),
+      constexpr int PER = decltype(n)::value;
+      // rows of more threads than kFwdThreads hold four blocks of 128 columns a half warp
+      auto kern = PER == 4 && r.tpr > kFwdThreads ? rms_fwd_kernel<T, P, decltype(vv)::value, PER, PER == 4>
+                                                  : rms_fwd_kernel<T, P, decltype(vv)::value, PER, false>;
+      return launch_pdl(kern, dim3((unsigned)(((int64_t)c.N + r.rows - 1) / r.rows)),
                         dim3(r.tpr * r.rows), 0, s, static_cast<const T*>(x), ldx, static_cast<const T*>(residual), ldr,
                         static_cast<const P*>(weight), static_cast<T*>(h), static_cast<T*>(y), codes, scales, rstd, c.N,
                         c.H, r.nb, r.tpr, c.eps);
