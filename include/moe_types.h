@@ -1,6 +1,6 @@
 /*
  * moe_types.h -- element types of the layer operators (moe_norm.h, moe_embed.h, moe_scores.h,
- * moe_distill.h), passed as int32_t beside an untyped pointer.
+ * moe_distill.h, moe_blocks8.h, moe_linear.h, moe_rmsnorm.h), passed as int32_t beside an untyped pointer.
  */
 #ifndef TOP_SOFTMAX_ROUTER_MOE_TYPES_H_
 #define TOP_SOFTMAX_ROUTER_MOE_TYPES_H_
