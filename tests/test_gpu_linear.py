@@ -268,3 +268,42 @@ def test_a_thread_of_its_own(M):
         t.start()
         t.join()
     assert len(got) == 2 and all(torch.equal(p, q) for g in got for p, q in zip(g, want))
+
+
+CLUSTERS = 76                                    # of a GB300
+
+
+def shares_of(tiles, blocks):
+    """Into how many shares a tile of so many K blocks is split."""
+    return max(1, min(CLUSTERS // tiles, blocks // 4)) if tiles else 1
+
+
+@pytest.mark.parametrize("n,K,O", [(2500, 1536, 1536), (2500, 2560, 2560)])
+def test_weight_gradients_of_several_accumulators(M, n, K, O):
+    """More than 1024 rows to a share, so that dw's fp32 sums over accumulators are formed; with two shares to a tile (36
+    tiles), and with more tiles than clusters (100)."""
+    tiles, blocks = -(-K // 256) * -(-O // 256), -(-n // 64)
+    per = -(-blocks // shares_of(tiles, blocks))
+    assert per > 16 and (tiles > CLUSTERS or shares_of(tiles, blocks) > 1)
+    check(M, Case(M, n, K, O), forward=False)
+    check(M, Case(M, n, K, O, x8=True), forward=False, dw_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("counts", [None, [257, 300, 513, 0, 300], [256] * 9])
+def test_clusters_with_several_full_tiles(M, kind, counts):
+    """y and dx of more than two rounds of tiles (a cluster's second and third accumulator, rows of both CTAs), each of more
+    than four K blocks."""
+    n = 2300 if counts is None else sum(counts)
+    off = None if counts is None else ends(counts)
+    rows = sum(-(-c // 256) for c in (counts or [n]))
+    for K, O in ((1040, 4112), (4112, 1040)):
+        c = Case(M, n, K, O, off, **KINDS[kind], seed=n)
+        u = c.unit(M)
+        y = u.forward(c.x, c.w, c.off, c.xs, c.ws)
+        near(y, *R.linear(c.X, c.W, c.off_host), K, 2.0 ** -8)
+        dx, _ = u.backward(c.x, c.w, c.dy, c.off, c.xs, c.ws, want_dw=False)
+        near(dx, *R.linear_dx(c.D, c.W, c.off_host), O, 2.0 ** -8)
+        u.check()
+        assert rows * -(-max(K, O) // 256) > 2 * CLUSTERS and min(K, O) > 4 * 128
+        del u
