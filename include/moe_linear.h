@@ -16,7 +16,7 @@
  *
  *   y[n, o] = sum over blocks b of 2^(sx[n, b] + sw[o / 128, b]) sum over k in b of cx[n, k] cw[o, k]
  *
- * with fp32 sums in the tensor cores; dx takes dy packed as moe_blocks8_pack does, along O; dW takes dy as it is and
+ * dx takes dy packed as moe_blocks8_pack does, along O; dW takes dy as it is and
  * the values that x's codes stand for.  The backward also takes x in codes beside bf16 weights: an activation
  * checkpoint in 8 bits.
  *
@@ -26,6 +26,8 @@
  *   - shapes: N >= 0, 1 <= E <= 1024, K and O multiples of 16 up to 2^20.  Else MOE_ERR_UNSUPPORTED_SHAPE.
  *   - offsets [E + 1] int32 on the device: 0 <= offsets[0] <= .. <= offsets[E] <= N.  Others are reported as
  *     MOE_ERR_DEVICE_CHECK in the workspace status word (moe_check_status); nothing is then written.
+ *   - sums are fp32, over accumulators of the tensor cores, which cut their additions off towards zero: 1024 products of
+ *     bf16 or 4096 of codes go to each, whatever the length of the sum.
  *   - repeated calls on the same inputs give the same bits.  A row's y and dx may depend in their last bits on how
  *     many rows the call has (few rows are split along K).
  *   - a wait that runs out (moe_set_wait_limit_ns) is reported as MOE_ERR_TIMEOUT; outputs are then of no use, and the

@@ -307,3 +307,49 @@ def test_clusters_with_several_full_tiles(M, kind, counts):
         u.check()
         assert rows * -(-max(K, O) // 256) > 2 * CLUSTERS and min(K, O) > 4 * 128
         del u
+
+
+def values8(codes, scales):
+    """The fp64 values of codes [n, k] with one scale for 128 of a row, or [E, o, k] with one for 128 x 128."""
+    s = scales.double().repeat_interleave(128, -1)[..., :codes.shape[-1]]
+    return codes.double() * (s if codes.dim() == 2 else s.repeat_interleave(128, 1)[:, :codes.shape[1]])
+
+
+@pytest.mark.parametrize("what", ["y", "dx"])
+@pytest.mark.parametrize("kind,length", [("bf16", 1 << 16), ("e4m3", 1 << 17)])
+def test_long_sums_are_not_cut_to_one_side(M, kind, length, what):
+    """Positive terms, as many tiles as clusters and one more (so that none is split): the sums' mean error, one-sided where
+    additions are cut off towards zero.  An accumulator takes 1024 products in bf16, 64 additions (4096 in e4m3, 128), each
+    off by at most 2^-23 of it, its products by another 32 such steps; the accumulators are added in fp32.  Against the
+    correctly rounded value an error of mean B moves the share B / 2^-8 of the values by a step of at most 2^-7: five sigmas
+    of that beside it."""
+    n, few = 77 * 256, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def positive(*shape):
+        v = torch.rand(*shape, device="cuda", generator=g, dtype=torch.bfloat16).add_(0.5)
+        return v.mul_(torch.exp2(torch.rand(*shape[:-1], 1, device="cuda", generator=g)).bfloat16())   # spread over a binade
+
+    a = positive(n, length)
+    K, O = (length, few) if what == "y" else (few, length)
+    b = positive(1, few, length) / length                      # [1, few, length]: W itself for y, its transpose for dx
+    w = b.contiguous() if what == "y" else b.transpose(1, 2).contiguous()
+    u = M.ExpertLinear(M.ExpertLinearConfig(N=n, K=K, O=O, blocks8=kind == "e4m3" and what == "dx"))
+    ck = M.Checkpoint8(M.Checkpoint8Config(N=n, H=length))
+    codes, scales = ck.pack(a) if kind == "e4m3" else (None, None)
+    wc, ws = M.pack_weight8(w) if kind == "e4m3" else (w, None)
+    if what == "y":
+        got = u.forward(a if kind == "bf16" else codes, wc, None, scales, ws)
+    else:
+        got = u.backward(None, wc, a, None, None, ws, want_dw=False)[0]
+    u.check()
+    W = (w.double() if kind == "bf16" else values8(wc, ws))[0]
+    W = W.t() if what == "y" else W                            # [length, few]
+    total = 0.0
+    for r in range(0, n, 1024):
+        at = slice(r, min(n, r + 1024))
+        ref = (a[at].double() if kind == "bf16" else values8(codes[at], scales[at])) @ W
+        total += ((got[at].double() - ref.bfloat16().double()) / ref).sum().item()
+    products, additions = (1024, 64) if kind == "bf16" else (4096, 128)
+    bound = (additions + 32) * 2.0 ** -23 + length / products * 2.0 ** -24
+    assert abs(total / got.numel()) <= bound + 5 * (bound * 2.0 ** -6 / got.numel()) ** 0.5

@@ -81,10 +81,15 @@ struct LinGemm {
 constexpr int kLinClusters = 76;   // at most this many clusters run (two dies x 76 SMs in pairs)
 constexpr int kLinBand = 8;        // row tiles that are worked on together: their rows and a few column tiles of W stay in L2
 constexpr int kFewRows = 32;       // tiles of no more rows load no more of A (other experts' rows would come with them)
-// The tensor cores cut each addition to an accumulator off towards zero: dW sums 1024 rows to an accumulator and adds
-// those in fp32 registers, so that the loss does not grow with the rows.
-// (Relative error of dW over 1000 rows 9.8e-7; plain fp32 sums have 6.5e-7.)
-constexpr int kDwShare = 16;       // K blocks of 64 rows
+// The tensor cores cut each addition to an accumulator off towards zero, so that long sums come out too small.  An
+// accumulator therefore takes so many K blocks, of four additions each, at most, and the epilogue adds a tile's
+// accumulators in fp32 registers: 1024 products of bf16; 4096 of codes, whose accumulators follow each other only once the
+// columns that they share are drained (and the scales of four blocks come together).
+// Values of y that are not the correctly rounded ones, one accumulator over all of K -> these: bf16, K = 2048, 1.27e-3 ->
+// 7.1e-4; codes, K = 7168, 2.6e-4 -> 1.6e-4; sums in fp32 alone have 2.8e-4 and 0.9e-4.  dW over 1000 rows is 9.8e-7 off,
+// plain fp32 sums 6.5e-7.  What it costs: y up to 1 %, dx 2 to 3 (126976 rows over 64 experts of 2048 x 1408 433 -> 443 us).
+template <bool MX>
+constexpr int kAccBlocks = MX ? 32 : 16;
 
 struct LinSmem {
   static constexpr int HALF = 128 * 128;               // 16 KB: this CTA's rows of A, or its half of B
@@ -179,12 +184,6 @@ __host__ __device__ constexpr uint32_t instr_desc_mx(int M, int N, bool b_mn) {
   return ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 16 consecutive fp32 columns of tensor memory.
-__device__ __forceinline__ void tc_ld16(uint32_t taddr, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-  tc_add16(taddr, v);
-}
 // 16 values to a dense row: one 32-byte sector of bf16, two of fp32.
 __device__ __forceinline__ void lin_store16(const LinGemm& p, int64_t at, const float* v) {
   if (p.out32) {
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
       bool ok = true;
       for (int w = cluster; w < items && ok; w += clusters) {
         const LinTile t = lin_tile<MODE, MX>(p, offs, first, w, total, shares);
-        const int step = MODE == LIN_DW ? kDwShare : max(1, t.kb1 - t.kb0);
+        constexpr int step = kAccBlocks<MX>;
         // one accumulator after the other (an empty share still passes its accumulator on)
         for (int k0 = t.kb0; ok && (k0 < t.kb1 || k0 == t.kb0); k0 += step, ++it) {
           const int acc = it & 1;
@@ -576,13 +575,10 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
       const bool some = __ballot_sync(0xffffffffu, in) != 0;   // any row of this warp's 32
       const int c0 = t.nt * 256 + half * 128, width = min(128, p.cols - c0);   // a multiple of 16
       const bool none = t.kb0 == t.kb1;
-      const int step = MODE == LIN_DW ? kDwShare : max(1, t.kb1 - t.kb0);
-      const int accs = MODE == LIN_DW ? max(1, (t.kb1 - t.kb0 + step - 1) / step) : 1;
-      float sum[MODE == LIN_DW ? 128 : 1];   // of the accumulators so far
-      if constexpr (MODE == LIN_DW) {
+      const int accs = max(1, (t.kb1 - t.kb0 + kAccBlocks<MX> - 1) / kAccBlocks<MX>);
+      float sum[128];                        // of the accumulators so far
 #pragma unroll
-        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-      }
+      for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
       // 16 columns from column c of this warp's half on: to the output, or to this share's place
       float4* part = reinterpret_cast<float4*>(p.part + ((int64_t)(w * 2 + (int)rank) * 8 + (warp - 2)) * 4096) + lane;
       auto leave = [&](int c, const float* v) {
@@ -613,52 +609,31 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
             else mbar_arrive_cluster(mapa_shared(tempty_bar(bar), 0));
           }
         };
-        if constexpr (MODE == LIN_DW) {
+        // MX: the first accumulator's last 32 columns are the second's first 32; they go first.
+        const bool shared_last = MX && half == 1 && acc == 0, shared_first = MX && half == 0 && acc == 1;
+        if (MX) {
           if (!none) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 16) tc_add16(tacc + c, sum + c);
-          }
-          release(acc);
-        } else {
-          // MX: the first accumulator's last 32 columns are the second's first 32
-          const bool shared_cols = MX && half == 1 - acc;
-          const int at = acc == 0 ? 96 : 0;
-          float v[16], u[16];
-          if (MX) {
-            if (shared_cols) {
-              tc_ld16(tacc + at, v);
-              tc_ld16(tacc + at + 16, u);
+            if (shared_first) {
+              tc_add16(tacc, sum);
+              tc_add16(tacc + 16, sum + 16);
             }
-            release(0);
-            if (none) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = u[j] = 0.0f;
-            }
-            if (shared_cols) {
-              leave(at, v);
-              leave(at + 16, u);
+            if (shared_last) {
+              tc_add16(tacc + 96, sum + 96);
+              tc_add16(tacc + 112, sum + 112);
             }
           }
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            if (shared_cols && c == at) continue;
-            tc_ld16(tacc + c, v);
-            tc_ld16(tacc + c + 16, u);
-            if (none) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = u[j] = 0.0f;
-            }
-            leave(c, v);
-            leave(c + 16, u);
-          }
-          if (!MX) release(acc);
+          release(0);
         }
+        if (!none) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 16)
+            if (!(c < 32 && shared_first) && !(c >= 96 && shared_last)) tc_add16(tacc + c, sum + c);
+        }
+        if (!MX) release(acc);
       }
       if (!ok) break;
-      if constexpr (MODE == LIN_DW) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) leave(c, sum + c);
-      }
+      for (int c = 0; c < 128; c += 16) leave(c, sum + c);
       if (shares > 1 && some) {
         // The last of a piece's shares adds them up, in their order.
         __threadfence();
