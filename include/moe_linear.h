@@ -31,7 +31,7 @@
  *   - repeated calls on the same inputs give the same bits.  A row's y and dx may depend in their last bits on how
  *     many rows the call has (few rows are split along K).
  *   - a wait that runs out (moe_set_wait_limit_ns) is reported as MOE_ERR_TIMEOUT; outputs are then of no use, and the
- *     workspace has to be cleared (to zeros, as at the start) before the next call.
+ *     workspace's first fwd_bytes have to be cleared (to zeros, as at the start) before the next call.
  */
 #ifndef TOP_SOFTMAX_ROUTER_MOE_LINEAR_H_
 #define TOP_SOFTMAX_ROUTER_MOE_LINEAR_H_

@@ -353,3 +353,23 @@ def test_long_sums_are_not_cut_to_one_side(M, kind, length, what):
     products, additions = (1024, 64) if kind == "bf16" else (4096, 128)
     bound = (additions + 32) * 2.0 ** -23 + length / products * 2.0 ** -24
     assert abs(total / got.numel()) <= bound + 5 * (bound * 2.0 ** -6 / got.numel()) ** 0.5
+
+
+def test_a_check_clears_on_the_stream_it_checked(M):
+    """check(stream) while the current stream is busy: what a later call on `stream` reports is not wiped."""
+    from top_softmax_router_gb300._lib import MoeError
+    u = M.ExpertLinear(M.ExpertLinearConfig(N=10, K=64, O=64, E=3))
+    x, w = torch.randn(10, 64, device="cuda").bfloat16(), torch.randn(3, 64, 64, device="cuda").bfloat16()
+    bad = torch.tensor([0, 5, 4, 10], dtype=torch.int32, device="cuda")
+    side, busy = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    u.forward(x, w, bad, stream=side)
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(400_000_000)             # cycles: a fifth of a second
+        with pytest.raises(MoeError):
+            u.check(stream=side)
+        u.forward(x, w, bad, stream=side)
+    torch.cuda.synchronize()
+    with pytest.raises(MoeError):
+        u.check(stream=side)
+    u.check()

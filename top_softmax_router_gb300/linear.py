@@ -42,7 +42,8 @@ class ExpertLinear:
     def __init__(self, cfg: ExpertLinearConfig, device="cuda"):
         self.cfg = cfg
         self._c = _args.Structs(cfg)
-        self.ws = _args.workspace(max(linear_workspace_bytes(cfg)), device)
+        self._shared, most = linear_workspace_bytes(cfg)   # what both passes use comes first
+        self.ws = _args.workspace(most, device)
 
     def _x(self, x, scales):
         c = self.cfg
@@ -117,9 +118,11 @@ class ExpertLinear:
 
     def check(self, stream=None) -> None:
         """Raises if a call since the last check met offsets that are none, or a wait ran out; the workspace is then as
-        new."""
+        new for calls on `stream`, the one the unit's calls ran on."""
         from .api import check_status
-        code = check_status(self.ws, stream)
+        on = _args.On(stream, self.ws.device)
+        code = check_status(self.ws, on.handle)
         if code:
-            self.ws.zero_()
+            with torch.cuda.stream(on.stream):     # before the next call there, whatever the current stream
+                self.ws[:self._shared].zero_()     # the shares and their counters; nothing else has to be zero
         check(code, "device status")
