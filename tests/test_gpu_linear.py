@@ -373,3 +373,18 @@ def test_a_check_clears_on_the_stream_it_checked(M):
     with pytest.raises(MoeError):
         u.check(stream=side)
     u.check()
+
+
+@pytest.mark.parametrize("kind,K,O", [("e4m3", 7168, 2048), ("bf16", 3584, 2048), ("bf16", 7168, 2048), ("e4m3", 2048, 256), ("bf16", 320, 272)])
+def test_no_share_is_empty(M, kind, K, O):
+    """A tile's shares have K blocks each: as many places of the workspace are written as there are such shares."""
+    c = Case(M, 8, K, O, **KINDS[kind])
+    u = c.unit(M)
+    places = u.ws[:M.linear_workspace_bytes(u.cfg)[0]][-CLUSTERS * 256 * 256 * 4:].view(torch.float32).view(CLUSTERS, -1)
+    places.fill_(float("nan"))
+    near(u.forward(c.x, c.w, None, c.xs, c.ws), *R.linear(c.X, c.W, c.off_host), K, 2.0 ** -8)
+    tiles, blocks = -(-O // 256), -(-K // (128 if kind == "e4m3" else 64))
+    per = -(-blocks // shares_of(tiles, blocks))
+    per = -(-per // 4) * 4 if kind == "e4m3" else per
+    shares = -(-blocks // per)
+    assert (~torch.isnan(places)).any(dim=1).sum().item() == (tiles * shares if shares > 1 else 0)

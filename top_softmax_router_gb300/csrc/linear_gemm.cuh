@@ -121,6 +121,13 @@ __device__ __forceinline__ void lin_band(int w, int tiles_m, int tiles_n, int* m
   *mt = b * kLinBand + (rem - *nt * in_band);
 }
 
+// K blocks of each of a tile's shares but the last.
+template <bool MX>
+__device__ __forceinline__ int lin_share(int nk, int shares) {
+  const int per = (nk + shares - 1) / shares;
+  return MX ? (per + 3) & ~3 : per;    // the scales come four K blocks at a time
+}
+
 template <int MODE, bool MX>
 __device__ __forceinline__ LinTile lin_tile(const LinGemm& p, const int* offs, const int* first, int w, int total, int shares) {
   LinTile t;
@@ -150,8 +157,7 @@ __device__ __forceinline__ LinTile lin_tile(const LinGemm& p, const int* offs, c
     t.rows = min(256, n - 256 * m);
     nk = p.nk;
   }
-  int per = (nk + shares - 1) / shares;
-  if (MX) per = (per + 3) & ~3;        // the scales come four K blocks at a time
+  const int per = lin_share<MX>(nk, shares);
   t.kb0 = min(nk, t.share * per);
   t.kb1 = min(nk, t.kb0 + per);
   return t;
@@ -307,7 +313,11 @@ __global__ void __launch_bounds__(LinSmem::threads(MX), 1)
   const int total = bad ? 0 : MODE == LIN_DW ? p.E * p.tiles_m * p.tiles_n : first[p.E];
   const int blocks = MODE == LIN_DW ? (*most + 63) >> 6 : p.nk;
   // Shares of a tile: as many as there are clusters for, of four K blocks at least (of 128 bytes: 128 KB of a tile).
-  const int shares = total > 0 ? max(1, min(min(clusters, kLinClusters) / total, blocks >> 2)) : 1;
+  int shares = total > 0 ? max(1, min(min(clusters, kLinClusters) / total, blocks >> 2)) : 1;
+  if (MODE != LIN_DW && shares > 1) {              // as many as have K blocks (in dW that is each expert's own matter)
+    const int per = lin_share<MX>(blocks, shares);
+    shares = (blocks + per - 1) / per;
+  }
   const int items = total * shares;
 
   if (warp == 0) {
