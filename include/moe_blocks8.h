@@ -13,7 +13,8 @@
  * so that a value of ordinary size is off by at most 2^-4 of itself, one below 2^-6 x scale by at most 2^-10 x scale.
  * Because the scale is a power of two, the division is exact and code x scale is a bf16 number without rounding (where
  * it is not below bf16's range).  NaN and infinities become NaN codes and leave the others of their block alone.
- * Magnitudes above 240 x 2^120, of fp32 or bf16, become that (the next code would be an infinity).
+ * Magnitudes above 240 x 2^120, of fp32 or bf16, become that (the next code would be an infinity), and so do those above
+ * 240 x 2^8 of a block of fp16 rows whose scale is 2^8: what is packed in a type is finite when it is restored in it.
  *
  * Conventions are those of moe.h, and: x has type MOE_TYPE_* and rows `ldx` elements apart; codes and scales are dense
  * ([N][H] and [N][ceil(H / 128)] bytes).  Pointers need only their element's alignment; rows that lie on 16 bytes take

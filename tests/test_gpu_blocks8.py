@@ -112,3 +112,17 @@ def test_a_large_checkpoint(M):
     rc, rs = R.pack(host(x[-3:]))
     assert np.array_equal(host(c[-3:]), rc) and np.array_equal(host(s[-3:]), rs)
     assert np.array_equal(host(u.unpack(c, s)[-3:]), R.unpack(rc, rs))
+
+
+def test_fp16_at_the_top_of_its_range(M):
+    """The finite fp16 values whose nearest code would stand for 65536, an infinity there: restored in fp16 they are finite,
+    and off by at most 2^-4 as every other."""
+    top = torch.arange(0x7A00, 0x7C00, dtype=torch.int16).view(torch.float16)      # 49152 .. 65504
+    x = torch.stack([top.view(4, 128), -top.view(4, 128)]).view(8, 128)
+    x[5, 64:] = 1.0
+    u = M.Checkpoint8(M.Checkpoint8Config(N=8, H=128))
+    c, s = u.pack(x.cuda())
+    rc, rs = R.pack(host(x))
+    assert np.array_equal(host(s), rs) and np.array_equal(host(c), np.where((rs == 2.0 ** 8) & (np.abs(rc) == 256), np.sign(rc) * 240, rc))
+    y = host(u.unpack(c, s, torch.float16))
+    assert np.all(np.isfinite(y)) and np.all(np.abs(y - host(x)) <= 2.0 ** -4 * np.abs(host(x)))

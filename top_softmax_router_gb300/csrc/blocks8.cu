@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int j = 0; j < kBatch; ++j) {
     const int byte = block_scale_byte(m[j]);
     if (valid[j]) {
-      store_codes8<VEC>(codes + to[j], lane16, valid[j], block_codes(f[j], byte, infinite));
+      store_codes8<VEC>(codes + to[j], lane16, valid[j], block_codes(f[j], byte, infinite, kTopByte<T>));
       if (lane16 == 0) scales[first + j] = (uint8_t)byte;
     }
   }
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int r = sub + 16 * j;
-    if (r < rows) store_codes8<VEC>(codes + base + (int64_t)r * K, lane16, valid, block_codes(f[j], byte, infinite));
+    if (r < rows) store_codes8<VEC>(codes + base + (int64_t)r * K, lane16, valid, block_codes(f[j], byte, infinite, kTopByte<float>));
   }
 }
 

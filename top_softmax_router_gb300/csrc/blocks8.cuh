@@ -19,8 +19,10 @@ __device__ __forceinline__ float block_scale_inverse(int byte) { return __uint_a
 __device__ __forceinline__ float block_scale(int byte) {
   return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)byte << 23);
 }
-// Largest code: at byte 247 the code above 240, 256 x 2^120, would stand for an infinity.
-__device__ __forceinline__ float block_code_limit(int byte) { return byte >= 247 ? 240.0f : 448.0f; }
+// Scales from this byte on have codes above 240 that would stand for an infinity of the values' type: 256 x 2^120, of fp32 and
+// bf16, and 256 x 2^8 of fp16.
+template <class T>
+constexpr int kTopByte = std::is_same<T, f16>::value ? 135 : 247;
 
 __device__ __forceinline__ float finite_magnitude(float v) {
   const float a = fabsf(v);
@@ -123,8 +125,9 @@ __device__ __forceinline__ bool blocks_max(const f32x2 (&f)[PER][4], float (&m)[
   among_lanes();
   return true;
 }
-// A lane's eight codes.  infinite: there may be infinities (else the quotients are within the codes, but for byte 247).
-__device__ __forceinline__ uint2 block_codes(const f32x2 (&f)[4], int byte, bool infinite) {
+// A lane's eight codes.  infinite: there may be infinities (else the quotients are within the codes, but for bytes from `top`
+// on, whose codes end at 240).
+__device__ __forceinline__ uint2 block_codes(const f32x2 (&f)[4], int byte, bool infinite, int top) {
   const float inv = block_scale_inverse(byte);
   const f32x2 inv2(inv);
   uint32_t c[4];
@@ -132,8 +135,8 @@ __device__ __forceinline__ uint2 block_codes(const f32x2 (&f)[4], int byte, bool
   for (int i = 0; i < 4; ++i) {
     float a, b;
     mul2(f[i], inv2).get(a, b);
-    if (infinite || byte >= 247) {
-      const float lim = block_code_limit(byte);
+    if (infinite || byte >= top) {
+      const float lim = byte >= top ? 240.0f : 448.0f;
       a = fabsf(a) < INFINITY ? fminf(fmaxf(a, -lim), lim) : __uint_as_float(0x7FFFFFFFu);
       b = fabsf(b) < INFINITY ? fminf(fmaxf(b, -lim), lim) : __uint_as_float(0x7FFFFFFFu);
     }

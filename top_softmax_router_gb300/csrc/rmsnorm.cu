@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(WIDE ? kFwdWide : kFwdThreads, WIDE ? 1 : 4)
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int byte = block_scale_byte(m[i]);
-    const uint2 c = block_codes(f[i], byte, infinite);
+    const uint2 c = block_codes(f[i], byte, infinite, kTopByte<float>);
     if constexpr (VEC) {
       if (in[i]) *reinterpret_cast<uint2*>(codes + to + i * step) = c;
     } else {
