@@ -102,3 +102,41 @@ def test_a_first_derivative_is_the_unit_s(M, name):
     x.grad = None
     f().sum().backward()
     assert torch.equal(x.grad, a)
+
+
+class Linear:
+    """Products by expert of a unit made without room for the backward pass of operands in 8 bits, or with it."""
+
+    def __init__(self, M, blocks8=False):
+        self.cfg = M.ExpertLinearConfig(N=8, K=16, O=32, blocks8=blocks8)
+        self.calls = []
+
+    def forward(self, x, w, offsets, x_scales=None, w_scales=None):
+        self.calls.append("forward")
+        return x @ w[0].t()
+
+    def backward(self, x, w, dy, offsets, x_scales, w_scales, want_dx, want_dw, dw_dtype):
+        self.calls.append(("x" if x is not None else "no x", "scales" if x_scales is not None else "no scales", want_dx, want_dw))
+        return dy @ w[0] if want_dx else None, (dy.t() @ x)[None].to(dw_dtype) if want_dw else None
+
+
+def linear_inputs(dtype=torch.bfloat16):
+    return torch.randn(8, 16).bfloat16(), torch.randn(1, 32, 16).to(dtype)
+
+
+def test_what_the_backward_pass_could_not_do_is_refused_before_the_forward(M):
+    """Weights in fp16, in which no gradient is made, and units without room for operands in 8 bits."""
+    x, w = linear_inputs(torch.float16)
+    room, none = Linear(M, True), Linear(M)
+    with pytest.raises(TypeError, match="w: expected bfloat16 or float32"):
+        M.expert_linear(x, w.requires_grad_(), room, keep="blocks8")
+    with pytest.raises(TypeError, match="w: expected bfloat16 or float32"):
+        M.rms_norm_linear8(x, None, w, None, room)
+    x, w = linear_inputs()
+    for a, b, keep in ((x, w.clone().requires_grad_(), "checkpoint8"), (x, w.clone().requires_grad_(), "blocks8"),
+                       (x.clone().requires_grad_(), w, "blocks8")):
+        with pytest.raises(ValueError, match="blocks8"):
+            M.expert_linear(a, b, none, keep=keep)
+    with pytest.raises(ValueError, match="blocks8"):
+        M.rms_norm_linear8(x, torch.ones(16, requires_grad=True), w, None, none)
+    assert not room.calls and not none.calls

@@ -250,6 +250,16 @@ def rms_norm(x, weight, unit: RMSNorm, residual=None):
     return _RMSNorm.apply(x, residual, weight, unit)
 
 
+def _check_gradients8(w, unit: ExpertLinear, *others):
+    """Refuses, before the forward pass, what the backward pass could not do with operands in 8 bits."""
+    if not torch.is_grad_enabled():
+        return
+    if w.requires_grad and w.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("w: expected bfloat16 or float32, the types its gradient is made in")
+    if any(t is not None and t.requires_grad for t in (w, *others)) and not unit.cfg.blocks8:
+        raise ValueError("operands in 8 bits: the unit was made without blocks8")
+
+
 class _ExpertLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets, unit, keep):
@@ -279,9 +289,12 @@ class _ExpertLinear(torch.autograd.Function):
 def expert_linear(x, w, unit: ExpertLinear, offsets=None, keep="bf16"):
     """Differentiable product by expert over an ExpertLinear's workspace, x [n, K] and w [E, O, K] in bf16.  keep: "bf16"
     keeps x for the backward pass, "checkpoint8" keeps it in 8 bits (which dw then takes it from), "blocks8" also computes
-    y and dx in 8 bits, with w and dy packed in each pass (the two need a unit made with blocks8)."""
+    y and dx in 8 bits, with w (bf16 or fp32; fp16 only where it gets no gradient) and dy packed in each pass.  The two need
+    a unit made with blocks8 where gradients are asked for."""
     if keep not in ("bf16", "checkpoint8", "blocks8"):
         raise ValueError("keep: expected 'bf16', 'checkpoint8' or 'blocks8'")
+    if keep != "bf16":
+        _check_gradients8(w, unit, *([x] if keep == "blocks8" else []))
     return _ExpertLinear.apply(x, w, offsets, unit, keep)
 
 
@@ -318,4 +331,5 @@ def rms_norm_linear8(x, weight, w, norm: RMSNorm, linear: ExpertLinear, residual
     the backward pass): out, or with a residual (out, h).  x, residual and w in bf16; `linear` made with blocks8."""
     if x.dtype != torch.bfloat16:
         raise TypeError("x: expected bfloat16")
+    _check_gradients8(w, linear, x, weight, residual)
     return _RMSNormLinear8.apply(x, residual, weight, w, offsets, norm, linear)

@@ -102,7 +102,7 @@ class ExpertLinear:
             wp, wsp = self._w(w, w_scales)
         if (xs is not None or wsp is not None) and not c.blocks8:
             raise ValueError("operands in 8 bits: the unit was made without blocks8")
-        if dw_dtype not in (torch.bfloat16, torch.float32):
+        if want_dw and dw_dtype not in (torch.bfloat16, torch.float32):
             raise TypeError("dw_dtype: expected torch.bfloat16 or torch.float32")
         op = self._offsets(offsets)
         _args.here(self.ws.device, dy, offsets, *((x, x_scales) if want_dw else ()), *((w, w_scales) if want_dx else ()))
@@ -111,7 +111,7 @@ class ExpertLinear:
         dw = on.empty((c.E, c.O, c.K), dw_dtype, dy.device) if want_dw else None
         check(_lib.load().moe_linear_backward(
             self._c(n), xp, ldx, xs, wp, wsp, op, gp, dx.data_ptr() if want_dx else None,
-            dw.data_ptr() if want_dw else None, _args.TYPES[dw_dtype], self.ws.data_ptr(), self.ws.numel(), on.handle),
+            dw.data_ptr() if want_dw else None, _args.TYPES[dw_dtype] if want_dw else 0, self.ws.data_ptr(), self.ws.numel(), on.handle),
             "moe_linear_backward")
         on.uses(x, w, dy, offsets, x_scales, w_scales, self.ws)
         return dx, dw
