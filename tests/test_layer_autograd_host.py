@@ -140,3 +140,17 @@ def test_what_the_backward_pass_could_not_do_is_refused_before_the_forward(M):
     with pytest.raises(ValueError, match="blocks8"):
         M.rms_norm_linear8(x, torch.ones(16, requires_grad=True), w, None, none)
     assert not room.calls and not none.calls
+
+
+def test_a_checkpoint_is_only_made_for_the_weights_gradient(M):
+    """Packing x takes a GPU: on the host it would raise."""
+    x, w = linear_inputs()
+    unit = Linear(M)
+    y = M.expert_linear(x, w, unit, keep="checkpoint8")
+    assert torch.equal(y, x @ w[0].t()) and unit.calls == ["forward"]
+    with torch.no_grad():
+        assert torch.equal(M.expert_linear(x, w.clone().requires_grad_(), unit, keep="checkpoint8"), y)
+    a = x.clone().requires_grad_()
+    dy = torch.randn(8, 32).bfloat16()
+    dx, = torch.autograd.grad(M.expert_linear(a, w, unit, keep="checkpoint8"), a, dy)
+    assert torch.equal(dx, dy @ w[0]) and unit.calls[-1] == ("no x", "no scales", True, False)

@@ -265,7 +265,9 @@ class _ExpertLinear(torch.autograd.Function):
     def forward(ctx, x, w, offsets, unit, keep):
         xs = ws = None
         kept, held = x, w
-        if keep != "bf16":
+        if keep == "nothing":
+            kept = None
+        elif keep != "bf16":
             kept, xs = Checkpoint8(Checkpoint8Config(N=unit.cfg.N, H=unit.cfg.K)).pack(x)
         if keep == "blocks8":
             held, ws = pack_weight8(w)
@@ -293,7 +295,9 @@ def expert_linear(x, w, unit: ExpertLinear, offsets=None, keep="bf16"):
     a unit made with blocks8 where gradients are asked for."""
     if keep not in ("bf16", "checkpoint8", "blocks8"):
         raise ValueError("keep: expected 'bf16', 'checkpoint8' or 'blocks8'")
-    if keep != "bf16":
+    if keep == "checkpoint8" and not (torch.is_grad_enabled() and w.requires_grad):
+        keep = "nothing"                # x is kept for dw alone
+    elif keep != "bf16":
         _check_gradients8(w, unit, *([x] if keep == "blocks8" else []))
     return _ExpertLinear.apply(x, w, offsets, unit, keep)
 
