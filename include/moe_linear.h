@@ -23,7 +23,8 @@
  * Conventions are those of moe.h (codes, stream as void*, asynchronous, capturable, the caller owns every buffer), and:
  *   - x, dy, y and dx: bf16 (x: or codes); x may have a row stride (ldx elements, a multiple of 16 bytes).  dy, y, dx,
  *     W and the scales are dense.  Every matrix lies on 16 bytes, offsets on 4.
- *   - shapes: N >= 0, 1 <= E <= 1024, K and O multiples of 16 up to 2^20.  Else MOE_ERR_UNSUPPORTED_SHAPE.
+ *   - shapes: 0 <= N <= 2^31 - 4096, 1 <= E <= 1024, K and O multiples of 16 up to 2^20; with blocks8 N times the blocks of 128
+ *     of K or O below 2^31.  Else MOE_ERR_UNSUPPORTED_SHAPE.
  *   - offsets [E + 1] int32 on the device: 0 <= offsets[0] <= .. <= offsets[E] <= N.  Others are reported as
  *     MOE_ERR_DEVICE_CHECK in the workspace status word (moe_check_status); nothing is then written.
  *   - sums are fp32, over accumulators of the tensor cores, which cut their additions off towards zero: 1024 products of
@@ -46,6 +47,7 @@ extern "C" {
 #endif
 
 #define MOE_LINEAR_MAX_E 1024
+#define MOE_LINEAR_MAX_N (2147483647 - 4095)
 
 /* N rows (the call's), K columns of x, O of y, E experts.  blocks8: the workspace has room for the backward pass of
  * operands in 8 bits (dy's codes and x's values). */

@@ -153,3 +153,12 @@ def test_python_refuses_host_tensors_types_and_shapes(lib):
         lin.backward(None, None, torch.zeros(4, 32))
     with pytest.raises(TypeError, match="x: expected bfloat16"):
         M.rms_norm_linear8(torch.zeros(4, 8), None, None, rms, lin)
+
+
+@pytest.mark.parametrize("cfg,code", [((2 ** 31 - 4096, 16, 16, 1, 0), 0), ((2 ** 31 - 4095, 16, 16, 1, 0), SHAPE), ((2 ** 31 - 1, 16, 16, 3, 0), SHAPE),
+                                      ((2 ** 30, 144, 16, 1, 1), SHAPE), ((2 ** 30 - 1, 144, 16, 1, 1), 0), ((2 ** 30, 16, 144, 1, 1), SHAPE), ((2 ** 30, 144, 144, 1, 0), 0)])
+def test_linear_rows_that_32_bits_cannot_count(lib, cfg, code):
+    """A kernel's row, plus a tile, or plus the rows that all its warps zero in a step, has to stay below 2^31; so have the
+    blocks of an operand that is packed or restored."""
+    assert 2 ** 31 - 4096 + 76 * 16 + 256 < 2 ** 31
+    assert lib.load().moe_linear_workspace_bytes(ref(lib.LinearConfig(*cfg)), None, None) == code

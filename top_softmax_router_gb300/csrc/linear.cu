@@ -14,7 +14,9 @@ int linear_validate(const moe_linear_config* c) {
   if (!c || c->N < 0 || c->K < 1 || c->O < 1 || c->E < 1 || (c->blocks8 != 0 && c->blocks8 != 1)) return MOE_ERR_INVALID_ARG;
   constexpr int most = 1 << 20;
   if (c->E > MOE_LINEAR_MAX_E || c->K % 16 || c->O % 16 || c->K > most || c->O > most) return MOE_ERR_UNSUPPORTED_SHAPE;
-  // tiles are counted in 32 bits
+  if (c->N > MOE_LINEAR_MAX_N) return MOE_ERR_UNSUPPORTED_SHAPE;   // a row and the kernels' steps past it are counted in 32 bits,
+  if (c->blocks8 && c->N * up(std::max(c->K, c->O), MOE_BLOCK8) > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;   // and so are blocks
+  // and tiles
   const int64_t rows = c->N / 256 + c->E, wide = up(std::max(c->K, c->O), 256);
   if (rows * wide > INT32_MAX / 4 || c->E * up(c->K, 256) * up(c->O, 256) > INT32_MAX / 4) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
