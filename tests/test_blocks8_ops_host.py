@@ -162,3 +162,17 @@ def test_linear_rows_that_32_bits_cannot_count(lib, cfg, code):
     blocks of an operand that is packed or restored."""
     assert 2 ** 31 - 4096 + 76 * 16 + 256 < 2 ** 31
     assert lib.load().moe_linear_workspace_bytes(ref(lib.LinearConfig(*cfg)), None, None) == code
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """Their lower bits alone would be another shape."""
+    import top_softmax_router_gb300 as M
+    big = 2 ** 32 + 16
+    for make in (lambda: M.ExpertLinear(M.ExpertLinearConfig(N=big, K=16, O=16), device="cpu"),
+                 lambda: M.ExpertLinear(M.ExpertLinearConfig(N=4, K=big, O=16), device="cpu"),
+                 lambda: M.RMSNorm(M.RMSNormConfig(N=big, H=8), device="cpu"),
+                 lambda: M.LayerNorm(M.LayerNormConfig(N=big, H=8), device="cpu")):
+        with pytest.raises(ValueError, match="out of range"):
+            make()
+    with pytest.raises(ValueError, match="out of range"):
+        M.pack_weight8(torch.empty(1, dtype=torch.bfloat16).expand(2 ** 32 + 1, 1, 1))

@@ -66,28 +66,38 @@ class CeConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "V", "P")]
 
 
-class LayerNormConfig(ctypes.Structure):
+class _Checked(ctypes.Structure):
+    """Sizes past 32 bits raise; ctypes would keep their lower bits, and the call would see another shape."""
+
+    def __init__(self, *args):
+        for (name, kind), v in zip(self._fields_, args):
+            if kind is ctypes.c_int32 and not -2 ** 31 <= v < 2 ** 31:
+                raise ValueError(f"{name}: {v} is out of range")
+        super().__init__(*args)
+
+
+class LayerNormConfig(_Checked):
     _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
-class EmbedConfig(ctypes.Structure):
+class EmbedConfig(_Checked):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "V", "H", "padding_idx")] + [("scale", ctypes.c_float)]
 
 
-class ScoresConfig(ctypes.Structure):
+class ScoresConfig(_Checked):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "E", "k", "groups", "topk_groups", "group_top", "score",
                                               "renormalize")] + [("scale", ctypes.c_float)]
 
 
-class DistillConfig(ctypes.Structure):
+class DistillConfig(_Checked):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "V", "K", "P")] + [("temperature", ctypes.c_float)]
 
 
-class LinearConfig(ctypes.Structure):
+class LinearConfig(_Checked):
     _fields_ = [(n, ctypes.c_int32) for n in ("N", "K", "O", "E", "blocks8")]
 
 
-class RmsNormConfig(ctypes.Structure):
+class RmsNormConfig(_Checked):
     _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 

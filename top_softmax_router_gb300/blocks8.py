@@ -74,6 +74,8 @@ def pack_weight8(w, stream=None):
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise TypeError("w: expected a torch.Tensor of three dimensions")
     E, O, K = w.shape
+    if max(E, O, K) >= 2 ** 31:
+        raise ValueError(f"w: shape {tuple(w.shape)} is out of range")
     wp = _args.ptr(w, "w", _args.TYPES, (E, O, K))
     _args.here(w.device)
     on = _args.On(stream, w.device)
