@@ -3,7 +3,8 @@
 // A half warp holds blocks of 128 columns of a row, eight values a lane, so that a block's largest magnitude is four
 // shuffles away: PER blocks a half warp, TPR threads a row (whole warps), several rows a block of threads where rows are
 // short.  Rows stay in registers between the statistics and the output: x, the residual and the outputs pass memory once.
-// Both kernels are persistent, and load their next row while they work on this one where the registers allow it.
+// A block of the forward takes one row a row group and leaves; the backward is persistent, and loads its next row while it
+// works on this one where the registers allow it.
 #include <algorithm>
 
 #include "../../include/moe_blocks8.h"
@@ -20,13 +21,16 @@ constexpr int kFwdThreads = 224, kFwdWide = 512;
 constexpr int bwd_threads(int per) { return per <= 2 ? 448 : 512; }
 constexpr int kMaxRows = 8;
 
-// A row's warps leave their sums here, in turn, so that one barrier a row suffices; places without a warp hold 0.
+// A row's warps leave their sums here; places without a warp hold 0.  The backward's rows take two of them in turn, so that
+// one barrier a row suffices.
+template <int TURNS>
 struct RowSums {
-  float4 v[2][kMaxRows][4];
+  float4 v[TURNS][kMaxRows][4];
 };
-__device__ __forceinline__ void clear(RowSums& r) {
+template <int TURNS>
+__device__ __forceinline__ void clear(RowSums<TURNS>& r) {
   float4* p = &r.v[0][0][0];
-  for (int i = threadIdx.x; i < 2 * kMaxRows * 4; i += blockDim.x) p[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = threadIdx.x; i < TURNS * kMaxRows * 4; i += blockDim.x) p[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   __syncthreads();
 }
 // The sum over a row's threads (tpr of them, whole warps of row group `group`), in a fixed order, in every thread.
@@ -87,7 +91,7 @@ __global__ void __launch_bounds__(WIDE ? kFwdWide : kFwdThreads, WIDE ? 1 : 4)
                    uint8_t* __restrict__ scales, float* __restrict__ rstd, int N, int H, int nb, int tpr, float eps) {
   pdl_wait();
   pdl_trigger();
-  __shared__ RowSums sums;
+  __shared__ RowSums<1> sums;
   const RowPlace at(tpr, H);
   const int64_t row = (int64_t)blockIdx.x * at.rows + at.group;
   const bool there = row < N;        // of a row group, so of whole warps
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(bwd_threads(PER), 1)
   pdl_trigger();
   constexpr bool AHEAD = VEC && PER * (int)sizeof(T) <= 4;
   constexpr bool LATE = PER * (int)sizeof(T) > 8;   // dh is loaded when it is needed
-  __shared__ RowSums sums;
+  __shared__ RowSums<2> sums;
   extern __shared__ float cols[];    // [H] where a block holds several rows
   if (tpr > 32) clear(sums);
   const RowPlace at(tpr, H);
@@ -314,10 +318,11 @@ int rms_validate(const moe_rmsnorm_config* c) {
   return c->H > MOE_RMSNORM_MAX_H ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
 }
 
-// Threads of a row and rows of a block, by the row's blocks of 128 columns: a warp a row up to 1024 columns, then 32
-// values a thread.  Threads with fewer values need fewer registers, and more blocks of them run on a SM.
+// Threads of a row and rows of a block, by the row's blocks of 128 columns.  A half warp has one block up to 256 columns, two
+// up to 512 in the forward and 7168 in the backward, else four; a row has whole warps of them, one up to 512 columns (1024 in
+// the forward).  Threads with fewer values need fewer registers, and more blocks of them run on a SM.
 struct RmsShape {
-  int nb, per, tpr, rows, most;
+  int nb, per, tpr, rows;
 };
 RmsShape rms_shape(int H, bool forward) {
   RmsShape s;
@@ -325,10 +330,12 @@ RmsShape rms_shape(int H, bool forward) {
   s.per = s.nb <= 2 ? 1 : s.nb <= (forward ? 4 : 56) ? 2 : 4;
   s.tpr = ((s.nb + s.per - 1) / s.per * 16 + 31) / 32 * 32;
   s.rows = std::max(1, (forward ? kFwdThreads : 256) / s.tpr);
-  s.most = 304 * (4 / s.per);
   return s;
 }
-int rms_blocks(int N, const RmsShape& s) { return (int)std::min<int64_t>(s.most, ((int64_t)N + s.rows - 1) / s.rows); }
+// The backward's blocks of threads.
+int rms_blocks(int N, const RmsShape& s) {
+  return (int)std::min<int64_t>(304 * (4 / s.per), ((int64_t)N + s.rows - 1) / s.rows);
+}
 
 // f(T, P, VEC, PER) with compile-time values.
 template <class F>
