@@ -388,3 +388,52 @@ def test_no_share_is_empty(M, kind, K, O):
     per = -(-per // 4) * 4 if kind == "e4m3" else per
     shares = -(-blocks // per)
     assert (~torch.isnan(places)).any(dim=1).sum().item() == (tiles * shares if shares > 1 else 0)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_gradients_past_2_to_31_elements(M, kind):
+    """x, dy and dx of more than 2^31 elements: the last rows, and what they give dw."""
+    n, K, O = 1_100_000, 2048, 2048
+    g = torch.Generator().manual_seed(4)
+    x, dy = (torch.zeros(n, 2048, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w = (torch.randn(2, O, K, generator=g) * K ** -0.5).bfloat16().cuda()
+    x[-5:], dy[-5:] = torch.randn(5, K, generator=g).bfloat16().cuda(), torch.randn(5, O, generator=g).bfloat16().cuda()
+    off = torch.tensor([0, n - 3, n], dtype=torch.int32, device="cuda")
+    X, W, D, xs, ws = host(x[-5:]), host(w), host(dy[-5:]), None, None
+    d_dw = D
+    if kind == "e4m3":
+        X, W, D = R.unpack(*R.pack(X)), R.unpack_weight(*R.pack_weight(W)), R.unpack(*R.pack(D))
+        x, xs = M.Checkpoint8(M.Checkpoint8Config(N=n, H=K)).pack(x)
+        w, ws = M.pack_weight8(w)
+    u = M.ExpertLinear(M.ExpertLinearConfig(N=n, K=K, O=O, E=2, blocks8=kind == "e4m3"))
+    if kind == "e4m3":
+        y = u.forward(x, w, off, xs, ws)
+        near(y[-5:], *R.linear(X, W, [0, 2, 5]), K, 2.0 ** -8)
+        del y
+    dx, dw = u.backward(x, w, dy, off, xs, ws)
+    u.check()
+    near(dx[-5:], *R.linear_dx(D, W, [0, 2, 5]), O, 2.0 ** -8)
+    assert not dx[:-5].any()
+    near(dw, *R.linear_dw(d_dw, X, [0, 2, 5], 2), 5, 2.0 ** -24)
+
+
+def test_weights_past_2_to_31_elements(M):
+    """The last experts' rows and gradients."""
+    E, n, K, O = 520, 20, 2048, 2048
+    g = torch.Generator().manual_seed(5)
+    off_host = [0] * (E - 2) + [5, 5, 20]
+    x, dy = torch.randn(n, K, generator=g).bfloat16().cuda(), torch.randn(n, O, generator=g).bfloat16().cuda()
+    w = torch.zeros(E, O, K, dtype=torch.bfloat16, device="cuda")
+    w[-3:] = (torch.randn(3, O, K, generator=g) * K ** -0.5).bfloat16().cuda()
+    off = torch.tensor(off_host, dtype=torch.int32, device="cuda")
+    X, W, D, last = host(x), host(w[-3:]), host(dy), off_host[-4:]
+    u = M.ExpertLinear(M.ExpertLinearConfig(N=n, K=K, O=O, E=E))
+    near(u.forward(x, w, off), *R.linear(X, W, last), K, 2.0 ** -8)
+    dx, dw = u.backward(x, w, dy, off)
+    u.check()
+    near(dx, *R.linear_dx(D, W, last), O, 2.0 ** -8)
+    near(dw[-3:], *R.linear_dw(D, X, last, 3), n, 2.0 ** -24)
+    assert not dw[:-3].any()
+    wc, ws = M.pack_weight8(w)
+    rc, rs = R.pack_weight(W)
+    assert np.array_equal(host(wc[-3:]), rc) and np.array_equal(host(ws[-3:]), rs)

@@ -173,3 +173,41 @@ def test_gradients_against_differences(M):
             d[i, j] = step
             up, down = (host(rms.forward((x + k * d).cuda(), w.cuda())[0]) for k in (1, -1))
             assert abs(((up - down) * host(dy)).sum() / (2 * step) - host(dx)[i, j]) < 40 * 2.0 ** -15 + 1e-3
+
+
+def test_rows_past_2_to_31_elements(M):
+    """The last rows of an odd and of an aligned width, forward and backward."""
+    for h in (7168, 7169):
+        n = 300_000
+        last = inputs(3, h, "bf16", "fp32", seed=h)
+        x, r, dy, dh = (torch.zeros(n, h, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+        for t, v in zip((x, r, dy, dh), (last[0], last[1], last[3], last[4])):
+            t[-3:] = v.cuda()
+        w = last[2].cuda()
+        rms = M.RMSNorm(M.RMSNormConfig(N=n, H=h))
+        y, kept, rstd, codes, scales = rms.forward(x, w, r, want_codes=True)
+        del x, r
+        dx, dw = rms.backward(kept, w, rstd, dy, dh)
+        few = M.RMSNorm(M.RMSNormConfig(N=3, H=h))
+        want = few.forward(last[0].cuda(), w, last[1].cuda(), want_codes=True)
+        for p, q in zip((y, kept, rstd, codes, scales), want):
+            p, q = (t.view(torch.uint8) if t.element_size() == 1 else t for t in (p, q))
+            assert torch.equal(p[-3:], q)
+        want_dx, want_dw = few.backward(want[1], w, want[2], last[3].cuda(), last[4].cuda())
+        assert torch.equal(dx[-3:], want_dx) and not dx[:-3].any()
+        # three terms, each rounded once as a product and at most twice in a sum, in both orders
+        terms = np.abs(host(last[3]) * host(want[1]) * host(want[2])[:, None]).sum(axis=0)
+        assert np.all(np.abs(host(dw) - host(want_dw)) <= 6 * U * terms)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+def test_scales_are_the_oracles_but_at_borders(M, t):
+    """A block's scale is the definition's for a largest value that is 36 u of itself off, which moves it only where that
+    value lies at a border between two scales."""
+    x, r, w, _, _ = inputs(700, 1024, t, "fp32", seed=11)
+    _, h, rstd, _, scales = M.RMSNorm(M.RMSNormConfig(N=700, H=1024)).forward(x.cuda(), w.cuda(), r.cuda(), want_codes=True)
+    ry, _ = R.rms_forward(host(h), host(w), 1e-6)
+    top = np.abs(ry.reshape(700, 8, 128)).max(axis=2)
+    low, high = R.scale_of(top * (1 - 36 * U)), R.scale_of(top * (1 + 36 * U))
+    got = host(scales)
+    assert np.all((got == low) | (got == high)) and np.mean(low != high) < 1e-3
