@@ -332,7 +332,8 @@ class _RMSNormLinear8(torch.autograd.Function):
 
 def rms_norm_linear8(x, weight, w, norm: RMSNorm, linear: ExpertLinear, residual=None, offsets=None):
     """The product by expert, in 8 bits, of an RMS norm's output, which is never written but in 8 bits (and kept so for
-    the backward pass): out, or with a residual (out, h).  x, residual and w in bf16; `linear` made with blocks8."""
+    the backward pass): out, or with a residual (out, h).  x, residual and w in bf16; `linear` made with blocks8.  The norm
+    is of every row: what rows of no expert hold enters `weight`'s gradient where it is no number (0 x NaN)."""
     if x.dtype != torch.bfloat16:
         raise TypeError("x: expected bfloat16")
     _check_gradients8(w, linear, x, weight, residual)
