@@ -23,13 +23,13 @@
 // column 224, and the scales lie in columns 480 .. 511.  The 32 columns that the accumulators share are drained first;
 // the next tile's MMAs wait for that alone.
 //
-// Bound by the tensor cores where there are many rows: 16384 x 7168 x 2048 (481 GFLOP each) y 158 us, dx 169 in 8 bits
-// (3.0 and 2.8 PFLOP/s), y 260, dx 249, dW 260 in bf16 (1.85 to 1.93, the rate of a plain product); without any copy to wait
-// for the MMAs alone take 127 and 146, 220 and 219.  By tiles that are not full and by each tile's end where an expert has
-// a few hundred rows: 128 experts, 63488 x 4096 x 1536 (799 GFLOP) y 362 us, dx 406, dW 681, whose tiles are eight K blocks
-// and 64 KB of output a CTA.  By the weights' bytes where there are few: 128 rows over 128 experts of 4096 x 1536 in 8
+// Bound by the tensor cores where there are many rows: 16384 x 7168 x 2048 (481 GFLOP each) y 156 us, dx 171 in 8 bits
+// (3.1 and 2.8 PFLOP/s), y 264, dx 262, dW 271 in bf16 (1.77 to 1.84, near the rate of a plain product; each accumulator
+// over all of K: y 261, dx 254); without any copy to wait for, and with one accumulator, the MMAs alone take 127 and 146, 220
+// and 219.  By tiles that are not full and by each tile's end where an expert has a few hundred rows: 128 experts,
+// 63488 x 4096 x 1536 (799 GFLOP) y 358 us, dx 409, dW 678, whose tiles are eight K blocks and 64 KB of output a CTA.  By the weights' bytes where there are few: 128 rows over 128 experts of 4096 x 1536 in 8
 // bits 95 us, 5.1 TB/s; one expert of 7168 x 2048 and 8 rows 16 us, of which the weights' bytes are 2 and the rest is the
-// launch, the latency of eight K blocks and the join.
+// launch, the latency of a share's eight K blocks and the join of seven.
 //
 // Columns of the last tile past the matrix are computed and dropped: MMAs of fewer columns made 1408 of them no faster.
 // Experts taken in the order of their rows, to give the clusters the same number of K blocks, did not help dW either (64
